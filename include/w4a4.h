@@ -184,6 +184,55 @@ w4a4_status w8a8_linear(const void* X, const int8_t* Wq, const float* w_scale, i
                         const void* bias, void* Y, void* workspace, size_t workspace_bytes,
                         w4a4_stream_t stream);
 
+/* ---------------------------------------------------------------- around the INT8 product */
+/* What stands before and between the INT8 products of a transformer block:
+ * the residual's addition with the root-mean-square norm, and the gate of a
+ * gated MLP, each fused with the rotation and the per-token int8 quantization
+ * of the product that follows; and that product for any sizes.  The pages
+ * have no counterpart: their layers start from activations that are already
+ * normalised.
+ *
+ * These entry points take strided rows and three element types, and their
+ * conventions differ from the ones above in this:
+ *   - Row strides (ld*) count elements; every row is contiguous.  A stride is
+ *     not looked at when its matrix has one row.
+ *   - Activation tensors need the alignment of their element only; 16-byte
+ *     aligned bases and strides (in bytes) with K a multiple of 8 run faster.
+ *     Code tensors (int8) need 16-byte-aligned bases and strides that are
+ *     multiples of 16; the bytes between K and the stride are neither read
+ *     nor written.
+ *   - M = 0 is allowed: nothing is launched and no pointer is looked at.
+ *   - Non-finite values follow the formulas: a row with an infinity or a NaN
+ *     (or whose result overflows) gets the scale NaN and codes 0, so that
+ *     what its codes stand for is NaN throughout. */
+typedef enum { W4A4_DTYPE_BF16 = 0, W4A4_DTYPE_FP16 = 1, W4A4_DTYPE_FP32 = 2 } w4a4_dtype;
+
+/* Residual addition, root-mean-square norm, rotation, int8 quantization:
+ *   h = X + residual (fp32; residual NULL: h = X),
+ *   y = (h * (1 / sqrt(mean(h^2) + eps))) * gamma   (gamma NULL: ones),
+ *   per group of `group`: y <- H_g y (group 0: none),
+ *   x_scale = fl32(max |y| / 127), Xq = rint_half_even(fl32(y / x_scale)),
+ * and, where H is given, H = h rounded to the type.  The norm uses the
+ * unrounded h, and y is not rounded before it is quantized.
+ *   X [M, K], residual [M, K] or NULL, gamma [K] or NULL, H [M, K] or NULL:
+ *   `dtype`.  H may be X or residual itself (same base and stride), or share
+ *   no byte with them; Xq and x_scale share no byte with any input.
+ *   Xq [M, K] int8, x_scale [M] fp32.
+ * 1 <= K <= 32768; group in {0, 64, 128} and K a multiple of it (the codes
+ * then go to weights prepared with the same group); 1e-30 <= eps <= 1e30. */
+w4a4_status w8a8_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* residual, int64_t ldr,
+                                      const void* gamma, float eps, int M, int K, int group, w4a4_dtype dtype,
+                                      void* H, int64_t ldh, int8_t* Xq, int64_t ldq, float* x_scale,
+                                      w4a4_stream_t stream);
+
+/* SiLU(gate) * up, rotation, int8 quantization:
+ *   y = (gate / (1 + exp(-gate))) * up (fp32), then as above.
+ *   gate, up [M, K]: `dtype`; the two halves of one [M, 2 K] product are
+ *   given as two pointers with the same stride.  Shapes as above. */
+w4a4_status w8a8_silu_mul_quantize(const void* gate, int64_t ldg, const void* up, int64_t ldu, int M, int K,
+                                   int group, w4a4_dtype dtype, int8_t* Xq, int64_t ldq, float* x_scale,
+                                   w4a4_stream_t stream);
+
 /* ---------------------------------------------------------------- W4A8 twin */
 /* 4-bit weights with a zero point and 8-bit activations ("W4A4 and W4A8: The
  * New Quantization Toolkit" (renderbob.io), "Decoding the notation" and "How

@@ -25,6 +25,7 @@ __all__ = [
     "w4a4_lora_merge", "w4a4_gemm_gelu", "w4a4_linear_gelu", "w4a4_mlp", "w4a4_mlp_workspace_bytes",
     "w4a4_bake_lora_sr", "w4a4_get_device_error", "w4a4_selftest_wait_timeout", "w4a4_plan_rotate_quantize",
     "w4a4_plan_gemm_split",
+    "w8a8_add_rmsnorm_quantize", "w8a8_silu_mul_quantize",
     "DEVERR_WAIT_OPERANDS", "DEVERR_WAIT_SLOT", "DEVERR_WAIT_ACCUM", "DEVERR_WAIT_DRAIN",
 ]
 
@@ -61,6 +62,7 @@ def load_library():
             f"{_LIB_PATH} not built; run __graft_entry__.build() or python -m w4a4_int4_quantized_b200.build")
     lib = ctypes.CDLL(_LIB_PATH)
     P, I, Z, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
+    L, F = ctypes.c_int64, ctypes.c_float
     sig = {
         "w4a4_version": ([], I),
         "w4a4_status_string": ([I], ctypes.c_char_p),
@@ -75,6 +77,8 @@ def load_library():
         "w8a8_gemm": ([P, P, P, P, I, I, I, I, P, P, P, P], S),
         "w8a8_workspace_bytes": ([I, I], Z),
         "w8a8_linear": ([P, P, P, I, I, I, I, P, P, P, Z, P], S),
+        "w8a8_add_rmsnorm_quantize": ([P, L, P, L, P, F, I, I, I, I, P, L, P, L, P, P], S),
+        "w8a8_silu_mul_quantize": ([P, L, P, L, I, I, I, I, P, L, P, P], S),
         "w4a8_quantize_weights": ([P, I, I, I, P, P, P, P], S),
         "w4a8_gemm": ([P, P, P, P, P, I, I, I, I, P, P, P, P], S),
         "w4a8_workspace_bytes": ([I, I], Z),
@@ -249,6 +253,122 @@ def w8a8_linear(X, Wq, w_scale, group, bias=None, Y=None, workspace=None, stream
         _ptr(X), _ptr(Wq), _ptr(w_scale), M, N, K, group, _ptr(bias), _ptr(Y), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
     return Y
+
+
+# ---- around the INT8 product: strided rows, three element types -------------
+
+_DTYPES = None          # torch dtype -> W4A4_DTYPE_*, filled on first use
+
+
+def _dtype_code(dtype):
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    return _DTYPES.get(dtype, -1)      # -1: the library answers W4A4_ERR_INVALID_ARG
+
+
+def _require(ok, fn, status):
+    if not ok:
+        raise W4A4Error(fn, status)
+
+
+def _matrix(fn, t, shape, dtype, device):
+    """Data pointer and row stride (in elements) of a matrix whose rows are
+    contiguous; refuses another shape, element type or device."""
+    _require(t.dtype == dtype and t.device == device, fn, 1)
+    _require(t.shape == shape, fn, 2)
+    rows, cols = t.stride()
+    _require(cols == 1 or shape[1] == 1, fn, 2)
+    return t.data_ptr(), rows
+
+
+def _vector(fn, t, n, dtype, device):
+    _require(t.dtype == dtype and t.device == device, fn, 1)
+    _require(t.shape == (n,) and (n <= 1 or t.stride(0) == 1), fn, 2)
+    return t.data_ptr()
+
+
+class _launch_on:
+    """The raw stream to launch on, with its device current and (for a stream
+    that was given) outputs allocated on it."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = None
+        if device.type != "cuda":
+            raise W4A4Error("stream", 6)
+        if stream is not None:
+            self.guard = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        import torch
+        if self.guard is not None:
+            self.guard.__enter__()
+        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _codes_out(fn, Xq, M, K, device):
+    """A code matrix [M, K] with rows 16-byte aligned: (tensor, pointer, stride)."""
+    import torch
+    if Xq is None:
+        Xq = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
+    q, ldq = _matrix(fn, Xq, (M, K), torch.int8, device)
+    return Xq, q, ldq
+
+
+def w8a8_add_rmsnorm_quantize(X, gamma, eps, group=0, residual=None, H=None, Xq=None, x_scale=None, stream=None):
+    """Residual addition, RMS norm, rotation and per-token int8 quantization in
+    one kernel: (codes [M, K], scales [M], H).  X, residual, gamma (or None)
+    and H are bf16, fp16 or fp32, all of one type, rows of any stride.  H
+    (X + residual rounded to the type) is allocated when there is a residual
+    and None otherwise; it may be X or residual itself.  Codes allocated here
+    have their rows 16-byte aligned (a stride of K rounded up)."""
+    import torch
+    fn = "w8a8_add_rmsnorm_quantize"
+    M, K = X.shape
+    dt, dev = X.dtype, X.device
+    with _launch_on(dev, stream) as st:
+        x, ldx = _matrix(fn, X, (M, K), dt, dev)
+        r, ldr = (None, 0) if residual is None else _matrix(fn, residual, (M, K), dt, dev)
+        g = None if gamma is None else _vector(fn, gamma, K, dt, dev)
+        if H is None and residual is not None:
+            H = torch.empty((M, K), dtype=dt, device=dev)
+        h, ldh = (None, 0) if H is None else _matrix(fn, H, (M, K), dt, dev)
+        Xq, q, ldq = _codes_out(fn, Xq, M, K, dev)
+        if x_scale is None:
+            x_scale = torch.empty((M,), dtype=torch.float32, device=dev)
+        s = _vector(fn, x_scale, M, torch.float32, dev)
+        _check(fn, load_library().w8a8_add_rmsnorm_quantize(
+            x, ldx, r, ldr, g, eps, M, K, group, _dtype_code(dt), h, ldh, q, ldq, s, st))
+    return Xq, x_scale, H
+
+
+def w8a8_silu_mul_quantize(gate, up, group=0, Xq=None, x_scale=None, stream=None):
+    """SiLU(gate) * up, rotation and per-token int8 quantization in one kernel:
+    (codes [M, K], scales [M]).  gate and up are bf16, fp16 or fp32 [M, K],
+    rows of any stride: the halves of one [M, 2 K] product need no copy."""
+    import torch
+    fn = "w8a8_silu_mul_quantize"
+    M, K = gate.shape
+    dt, dev = gate.dtype, gate.device
+    with _launch_on(dev, stream) as st:
+        a, lda = _matrix(fn, gate, (M, K), dt, dev)
+        b, ldb = _matrix(fn, up, (M, K), dt, dev)
+        Xq, q, ldq = _codes_out(fn, Xq, M, K, dev)
+        if x_scale is None:
+            x_scale = torch.empty((M,), dtype=torch.float32, device=dev)
+        s = _vector(fn, x_scale, M, torch.float32, dev)
+        _check(fn, load_library().w8a8_silu_mul_quantize(
+            a, lda, b, ldb, M, K, group, _dtype_code(dt), q, ldq, s, st))
+    return Xq, x_scale
 
 
 def w4a8_quantize_weights(W, group, Wq=None, w_scale=None, w_zero=None, stream=None):

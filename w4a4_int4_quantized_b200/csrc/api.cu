@@ -336,6 +336,64 @@ w4a4_status w4a8_linear(const void* X, const uint8_t* Wq, const float* w_scale, 
   return w4a8_gemm(Xq, xs, Wq, w_scale, w_zero, M, N, K, group, bias, Y, nullptr, stream);
 }
 
+// ------------------------------------------------------------------ norm and gated activation to int8
+namespace {
+
+size_t dtype_bytes(w4a4_dtype t) { return t == W4A4_DTYPE_FP32 ? 4 : 2; }
+bool dtype_ok(w4a4_dtype t) { return t == W4A4_DTYPE_BF16 || t == W4A4_DTYPE_FP16 || t == W4A4_DTYPE_FP32; }
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// A row stride of a matrix with one row is not used.
+bool stride_ok(int M, int64_t ld, int64_t width) { return M <= 1 || ld >= width; }
+bool code_rows_ok(int rows, int64_t ld, int K) { return rows <= 1 || (ld >= K && ld % 16 == 0); }
+
+w4a4_status check_row_quantize(int M, int K, int group, w4a4_dtype dtype) {
+  if (!dtype_ok(dtype)) return W4A4_ERR_INVALID_ARG;
+  if (M < 0 || K < 1 || K > 32768) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  if (group != 0 && group != 64 && group != 128) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  if (group != 0 && K % group != 0) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  return W4A4_OK;
+}
+
+}  // namespace
+
+w4a4_status w8a8_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* residual, int64_t ldr,
+                                      const void* gamma, float eps, int M, int K, int group, w4a4_dtype dtype,
+                                      void* H, int64_t ldh, int8_t* Xq, int64_t ldq, float* x_scale,
+                                      w4a4_stream_t stream) {
+  w4a4_status s = check_row_quantize(M, K, group, dtype);
+  if (s != W4A4_OK) return s;
+  if (!(eps >= 1e-30f && eps <= 1e30f)) return W4A4_ERR_INVALID_ARG;
+  if (M == 0) return W4A4_OK;
+  if (!X || !Xq || !x_scale) return W4A4_ERR_INVALID_ARG;
+  if (!stride_ok(M, ldx, K) || (residual && !stride_ok(M, ldr, K)) || (H && !stride_ok(M, ldh, K)) ||
+      !code_rows_ok(M, ldq, K))
+    return W4A4_ERR_UNSUPPORTED_SHAPE;
+  const size_t es = dtype_bytes(dtype);
+  if (!aligned_to(X, es) || !aligned_to(residual, es) || !aligned_to(gamma, es) || !aligned_to(H, es) ||
+      !aligned16(Xq) || !aligned_to(x_scale, 4))
+    return W4A4_ERR_MISALIGNED;
+  if ((s = check_device()) != W4A4_OK) return s;
+  const RowQuantArgs a{X, residual, gamma, H, Xq, x_scale, ldx, ldr, ldh, ldq, M, K, group, eps};
+  return cuda_status(launch_row_quantize(a, false, (int)dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w4a4_status w8a8_silu_mul_quantize(const void* gate, int64_t ldg, const void* up, int64_t ldu, int M, int K,
+                                   int group, w4a4_dtype dtype, int8_t* Xq, int64_t ldq, float* x_scale,
+                                   w4a4_stream_t stream) {
+  w4a4_status s = check_row_quantize(M, K, group, dtype);
+  if (s != W4A4_OK) return s;
+  if (M == 0) return W4A4_OK;
+  if (!gate || !up || !Xq || !x_scale) return W4A4_ERR_INVALID_ARG;
+  if (!stride_ok(M, ldg, K) || !stride_ok(M, ldu, K) || !code_rows_ok(M, ldq, K)) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  const size_t es = dtype_bytes(dtype);
+  if (!aligned_to(gate, es) || !aligned_to(up, es) || !aligned16(Xq) || !aligned_to(x_scale, 4))
+    return W4A4_ERR_MISALIGNED;
+  if ((s = check_device()) != W4A4_OK) return s;
+  const RowQuantArgs a{gate, up, nullptr, nullptr, Xq, x_scale, ldg, ldu, 0, ldq, M, K, group, 0.0f};
+  return cuda_status(launch_row_quantize(a, true, (int)dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 // ------------------------------------------------------------------ runtime LoRA
 w4a4_status w4a4_lora_merge(const void* L1, const void* L2, int rank, const void* A, const void* B, int lora_rank,
                             float lora_scale, int K, int N, void* L1_out, void* L2_out, w4a4_stream_t stream) {

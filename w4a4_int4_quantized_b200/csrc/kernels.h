@@ -66,4 +66,20 @@ cudaError_t launch_lora_bake(const uint16_t* W, const uint16_t* A, const uint16_
 cudaError_t launch_lora_merge(const uint16_t* L1, const uint16_t* L2, int r, const uint16_t* A, const uint16_t* B,
                               int rl, float scale, int K, int N, uint16_t* L1o, uint16_t* L2o, cudaStream_t st);
 
+// Row operators ending in int8 codes (csrc/rowquant.cu).  Strides count
+// elements; A, B, H and gamma share one element type.
+struct RowQuantArgs {
+  const void* A;           // norm: x; silu: gate [M, K]
+  const void* B;           // norm: residual or null; silu: up
+  const void* gamma;       // norm: [K] or null
+  void* H;                 // norm: x + residual rounded to the type, or null (may be A or B itself)
+  int8_t* Xq;              // codes, rows ldq apart (ldq % 16 == 0)
+  float* x_scale;          // [M]
+  int64_t lda, ldb, ldh, ldq;
+  int M, K, group;
+  float eps;
+};
+// dtype: 0 bf16, 1 fp16, 2 fp32
+cudaError_t launch_row_quantize(const RowQuantArgs& a, bool silu, int dtype, cudaStream_t st);
+
 }  // namespace w4a4
