@@ -233,6 +233,22 @@ w4a4_status w8a8_silu_mul_quantize(const void* gate, int64_t ldg, const void* up
                                    int group, w4a4_dtype dtype, int8_t* Xq, int64_t ldq, float* x_scale,
                                    w4a4_stream_t stream);
 
+/* The int8 product with a scale per token and per output channel, for any
+ * sizes:
+ *   acc = sum_k Xq[m][k] Wq[n][k] (exact int32),
+ *   Y = ((acc * x_scale[m]) * w_scale[n]) * (1/g) + bias[n], fp32, rounded
+ *   once to `dtype`; g = `group`, or 1 for group 0.
+ * With bf16 out it gives w8a8_gemm's results bit for bit where both take the
+ * sizes; it has forms of its own for few tokens.
+ *   Xq [M, K], Wq [N, K] int8 (any code, -128 among them), x_scale [M],
+ *   w_scale [N] fp32, bias [N] or NULL and Y [M, N] of `dtype`.
+ *   Y shares no byte with any input.
+ * N >= 1, 1 <= K <= 131071, group in {0, 64, 128} (only its factor 1/g is
+ * applied here: K need not be a multiple of it). */
+w4a4_status w8a8_matmul(const int8_t* Xq, int64_t ldx, const float* x_scale, const int8_t* Wq, int64_t ldw,
+                        const float* w_scale, int M, int N, int K, int group, const void* bias, w4a4_dtype dtype,
+                        void* Y, int64_t ldy, w4a4_stream_t stream);
+
 /* ---------------------------------------------------------------- W4A8 twin */
 /* 4-bit weights with a zero point and 8-bit activations ("W4A4 and W4A8: The
  * New Quantization Toolkit" (renderbob.io), "Decoding the notation" and "How

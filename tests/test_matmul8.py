@@ -1,0 +1,252 @@
+"""The int8 product with token and channel scales (w8a8_matmul) against the
+same formula in 64 bits, and the run of the operators around it.
+
+Tolerance, with u = 2^-24 and h = half a step of the output type relative to
+the value: the product p = acc sx sw / g carries the conversion and two
+multiplications (3 u; 1/g is a power of two), the bias one addition (u of the
+sum), the store h (and half of the smallest fp16 step):
+|Y - Y64| <= 3 u |p| + (u + h (1 + 2^-7)) |Y64| + tiny; h's factor covers the
+store's rounding acting on a value already off by the other terms."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import w4a4_int4_quantized_b200 as w4
+
+from test_row_quantize import EPS, _data, _dt, _f64, _rows, check_codes, norm64, silu64
+
+U = 2.0 ** -24
+OK, INVALID, SHAPE, MISALIGNED = 0, 1, 2, 3
+
+
+# ------------------------------------------------------------------ refusals, no GPU
+@pytest.fixture(scope="module")
+def lib():
+    from w4a4_int4_quantized_b200 import build
+    build.build()
+    return w4.load_library()
+
+
+def test_refusals(lib):
+    f = lib.w8a8_matmul
+    names = ["Xq", "ldx", "sx", "Wq", "ldw", "sw", "M", "N", "K", "group", "bias", "dtype", "Y", "ldy", "st"]
+    good = dict(zip(names, [0x10000, 64, 0x20000, 0x30000, 64, 0x40000, 4, 24, 50, 0, 0x50000, 0, 0x60000, 24, None]))
+
+    def call(**kw):
+        return f(*[{**good, **kw}[n] for n in names])
+
+    for missing in ("Xq", "sx", "Wq", "sw", "Y"):
+        assert call(**{missing: None}) == INVALID
+    for dtype in (-1, 3):
+        assert call(dtype=dtype) == INVALID
+    for kw in (dict(M=-1), dict(N=0), dict(K=0), dict(K=131072, ldx=131072, ldw=131072), dict(group=1), dict(group=32),
+               dict(ldx=48), dict(ldx=72), dict(ldw=48), dict(ldw=65), dict(ldy=23)):
+        assert call(**kw) == SHAPE, kw
+    for kw in (dict(Xq=0x10008), dict(Wq=0x30001), dict(sx=0x20002), dict(sw=0x40001), dict(bias=0x50001),
+               dict(Y=0x60001), dict(Y=0x60002, dtype=2), dict(bias=0x50002, dtype=2)):
+        assert call(**kw) == MISALIGNED, kw
+    assert call(M=0, Xq=None, Y=None) == OK
+
+
+# ------------------------------------------------------------------ GPU
+gpu = pytest.mark.gpu
+
+
+def _codes(rows, K, seed, pad=0, full=False):
+    """int8 codes as a CUDA matrix with rows 16-byte aligned, `pad` more bytes apart."""
+    import torch
+    rng = np.random.default_rng(seed)
+    ld = (K + 15) // 16 * 16 + pad
+    buf = torch.full((rows, ld), 77, dtype=torch.int8, device="cuda")      # bytes past K must not count
+    c = np.full((rows, K), -128, np.int8) if full else rng.integers(-128, 128, (rows, K)).astype(np.int8)
+    buf[:, :K] = torch.from_numpy(c)
+    return buf[:, :K]
+
+
+def _case(M, N, K, seed, dtype, bias, pad=0, full=False):
+    import torch
+    rng = np.random.default_rng(seed)
+    sx = torch.from_numpy((0.01 + 0.05 * rng.random(M)).astype(np.float32)).cuda()
+    sw = torch.from_numpy((0.0002 + 0.0006 * rng.random(N)).astype(np.float32)).cuda()
+    v = torch.from_numpy(rng.standard_normal(N)).to(_dt(dtype)).cuda() if bias else None
+    return _codes(M, K, seed + 1, pad, full), sx, _codes(N, K, seed + 2, pad, full), sw, v
+
+
+def check_product(Y, Xq, sx, Wq, sw, g, v):
+    import torch
+    acc = (Xq.double() @ Wq.double().t()).cpu().numpy()       # exact: below 2^31
+    p = acc * _f64(sx)[:, None] * _f64(sw)[None, :] / (g or 1)
+    y = p + (0.0 if v is None else _f64(v)[None, :])
+    h = torch.finfo(Y.dtype).eps / 2
+    tiny = 2.0 ** -25 if Y.dtype == torch.float16 else 0.0
+    bound = 3 * U * np.abs(p) + (U + h * (1 + 2.0 ** -7)) * np.abs(y) + tiny
+    off = np.abs(_f64(Y) - y)
+    assert np.all(off <= bound), (float(np.max(off - bound)), np.argwhere(off > bound)[:5].tolist())
+
+
+SHAPES = [
+    # M, N, K, group
+    (1, 1, 1, 0), (1, 16, 64, 64), (1, 17, 16, 0), (3, 40, 65, 0), (1, 4096, 4096, 128), (2, 100, 1000, 0),
+    (8, 33, 511, 0), (9, 1000, 640, 64), (16, 257, 2047, 0), (17, 64, 128, 0), (31, 1001, 130, 0), (32, 520, 4100, 0),
+    (33, 7, 100, 0), (33, 256, 512, 0), (64, 129, 1025, 0), (65, 1024, 4096, 128), (100, 3000, 1000, 0),
+    (128, 512, 127, 0), (129, 1280, 2048, 0), (255, 255, 255, 0), (256, 2048, 1536, 64), (257, 333, 900, 0),
+    (300, 4104, 512, 0), (333, 1013, 2995, 0), (512, 5000, 384, 0), (1000, 1000, 1000, 0), (1025, 4352, 256, 128),
+    (2050, 2049, 130, 0), (5000, 24, 777, 0), (40, 20000, 264, 0), (700, 9000, 48, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M,N,K,group", SHAPES)
+def test_product(M, N, K, group, dtype):
+    import torch
+    Xq, sx, Wq, sw, v = _case(M, N, K, M + N + K, dtype, (M + N + K) % 2, pad=16 * (K % 3))
+    ldy = N + (N % 3)
+    buf = torch.full((M + 1, ldy), 5.0, dtype=_dt(dtype), device="cuda")
+    Y = buf[:M, :N]
+    out = w4.w8a8_matmul(Xq, sx, Wq, sw, group, v, Y=Y)
+    torch.cuda.synchronize()
+    assert out is Y
+    check_product(Y, Xq, sx, Wq, sw, group, v)
+    assert (buf[M] == 5).all() and (buf[:, N:] == 5).all()
+
+
+@gpu
+@pytest.mark.parametrize("M", [2, 30, 80, 300])
+def test_longest_sums_of_the_lowest_code(M):
+    import torch
+    Xq, sx, Wq, sw, _ = _case(M, 40, 131071, 3, "fp32", False, full=True)
+    Y = w4.w8a8_matmul(Xq, sx, Wq, sw, dtype=torch.float32)
+    torch.cuda.synchronize()
+    check_product(Y, Xq, sx, Wq, sw, 0, None)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(1, 256, 512), (20, 256, 512), (64, 256, 1024), (256, 520, 1024), (1000, 2048, 512)])
+def test_equal_to_the_layers_product(M, N, K):
+    import torch
+    Xq, sx, Wq, sw, v = _case(M, N, K, 9, "bf16", True)
+    want = w4.w8a8_gemm(Xq, sx, Wq, sw, 128, v)
+    got = w4.w8a8_matmul(Xq, sx, Wq, sw, 128, v)
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@gpu
+@pytest.mark.parametrize("M", [4, 40, 600])
+def test_non_finite_scales_stay_in_their_rows(M):
+    import torch
+    Xq, sx, Wq, sw, v = _case(M, 300, 256, 11, "bf16", True)
+    clean = w4.w8a8_matmul(Xq, sx, Wq, sw, 0, v).clone()
+    sx[1] = float("nan")
+    sx[2] = 0.0
+    Y = w4.w8a8_matmul(Xq, sx, Wq, sw, 0, v)
+    torch.cuda.synchronize()
+    assert torch.isnan(Y[1]).all() and torch.equal(Y[2], v)
+    keep = [m for m in range(M) if m not in (1, 2)]
+    assert torch.equal(Y[keep], clean[keep])
+
+
+@gpu
+@pytest.mark.parametrize("M", [1, 12, 40, 300])
+def test_rows_far_apart(M):
+    """Offsets past 2^31 bytes in the codes and past 2^31 elements in Y."""
+    import torch
+    N, K = 24, 100
+    Xq, sx, Wq, sw, _ = _case(M, N, K, 13, "bf16", False)
+    far = (1 << 31) // min(M, 20) // 16 * 16 + 16
+    bufw = torch.empty(((N - 1) * (1 << 27) + 128,), dtype=torch.int8, device="cuda")
+    W2 = bufw.as_strided((N, K), (1 << 27, 1))
+    W2.copy_(Wq)
+    bufx = torch.empty(((M - 1) * far + 128,), dtype=torch.int8, device="cuda")
+    X2 = bufx.as_strided((M, K), (far, 1)) if M > 1 else Xq
+    if M > 1:
+        X2.copy_(Xq)
+    bufy = torch.empty(((M - 1) * far + N,), dtype=torch.bfloat16, device="cuda")
+    Y2 = bufy.as_strided((M, N), (far, 1))
+    w4.w8a8_matmul(X2, sx, W2, sw, Y=Y2)
+    Y = w4.w8a8_matmul(Xq, sx, Wq, sw)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Y2)
+
+
+@gpu
+def test_no_rows_and_binding_refusals():
+    import torch
+    Xq, sx, Wq, sw, v = _case(4, 64, 128, 1, "bf16", True)
+    Y = w4.w8a8_matmul(Xq[:0], sx[:0], Wq, sw, 0, v)
+    assert Y.shape == (0, 64)
+    bad = [dict(x_scale=sx[:3]), dict(w_scale=sw[:8]), dict(bias=v.float()), dict(Y=torch.empty(4, 63, device="cuda")),
+           dict(Wq=Wq[:, :64]), dict(Xq=Xq.cpu()), dict(Wq=Wq.cpu()), dict(Xq=Xq.to(torch.uint8)), dict(group=3),
+           dict(dtype=torch.float64), dict(Y=torch.empty(64, 4, device="cuda", dtype=torch.bfloat16).t()),
+           dict(Wq=torch.zeros(64, 129, dtype=torch.int8, device="cuda")[:, :128])]
+    for kw in bad:
+        with pytest.raises(w4.W4A4Error):
+            w4.w8a8_matmul(**{**dict(Xq=Xq, x_scale=sx, Wq=Wq, w_scale=sw, bias=v), **kw})
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(5, 512, 768), (40, 512, 2048), (700, 2304, 640)])
+def test_two_streams_and_a_graph(M, N, K):
+    """Two streams at once, and a captured call replayed on new codes."""
+    import torch
+    Xq, sx, Wq, sw, v = _case(M, N, K, 17, "bf16", True)
+    X2 = _codes(M, K, 99)
+    want, want2 = (w4.w8a8_matmul(x, sx, Wq, sw, 0, v) for x in (Xq, X2))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        got.append((w4.w8a8_matmul(Xq, sx, Wq, sw, 0, v, stream=a), want))
+        got.append((w4.w8a8_matmul(X2, sx, Wq, sw, 0, v, stream=b), want2))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in got)
+    Y = torch.empty_like(want)
+    codes = Xq.clone(memory_format=torch.contiguous_format)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=a):
+        w4.w8a8_matmul(codes, sx, Wq, sw, 0, v, Y=Y)
+    for x, w in ((X2, want2), (Xq, want)):
+        codes.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, w)
+    del graph
+
+
+@gpu
+@pytest.mark.parametrize("M,D,F,group,dtype", [(1, 256, 640, 0, "bf16"), (7, 1000, 1500, 0, "fp16"),
+                                               (70, 512, 1408, 64, "bf16"), (600, 1024, 2816, 128, "bf16")])
+def test_gated_mlp(M, D, F, group, dtype):
+    """A gated MLP as a block runs it: norm -> gate | up -> SiLU * up -> down,
+    every step checked against 64 bits on the step's own inputs."""
+    import torch
+    dt = _dt(dtype)
+    rng = np.random.default_rng(5)
+    X, R = _rows(_data(M, D, 41), dt), _rows(_data(M, D, 42), dt)
+    gamma = _rows(1 + 0.1 * _data(1, D, 43), dt)[0]
+
+    def weights(n, k):
+        W = torch.from_numpy(rng.standard_normal((n, k)) * 0.05)
+        if group:
+            i = np.arange(group)
+            H = torch.from_numpy(1.0 - 2.0 * np.array([[bin(a & b).count("1") & 1 for b in i] for a in i]))
+            W = (W.reshape(n, k // group, group) @ H).reshape(n, k)
+        s = W.abs().amax(dim=1) / 127
+        q = torch.zeros((n, (k + 15) // 16 * 16), dtype=torch.int8)
+        q[:, :k] = torch.round(W / s[:, None]).to(torch.int8)
+        return q.cuda()[:, :k], s.float().cuda()
+
+    Wgu, sgu = weights(2 * F, D)
+    Wd, sd = weights(D, F)
+    q, s, h = w4.w8a8_add_rmsnorm_quantize(X, gamma, EPS, group, residual=R)
+    gu = w4.w8a8_matmul(q, s, Wgu, sgu, group, dtype=dt)
+    q2, s2 = w4.w8a8_silu_mul_quantize(gu[:, :F], gu[:, F:], group)
+    Y = w4.w8a8_matmul(q2, s2, Wd, sd, group, dtype=dt)
+    torch.cuda.synchronize()
+    _, y = norm64(_f64(X), _f64(R), _f64(gamma), EPS)
+    check_codes(y, group, 21, _f64(q), _f64(s))
+    check_product(gu, q, s, Wgu, sgu, group, None)
+    check_codes(silu64(_f64(gu[:, :F]), _f64(gu[:, F:])), group, 15, _f64(q2), _f64(s2))
+    check_product(Y, q2, s2, Wd, sd, group, None)

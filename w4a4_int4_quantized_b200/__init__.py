@@ -25,7 +25,7 @@ __all__ = [
     "w4a4_lora_merge", "w4a4_gemm_gelu", "w4a4_linear_gelu", "w4a4_mlp", "w4a4_mlp_workspace_bytes",
     "w4a4_bake_lora_sr", "w4a4_get_device_error", "w4a4_selftest_wait_timeout", "w4a4_plan_rotate_quantize",
     "w4a4_plan_gemm_split",
-    "w8a8_add_rmsnorm_quantize", "w8a8_silu_mul_quantize",
+    "w8a8_add_rmsnorm_quantize", "w8a8_silu_mul_quantize", "w8a8_matmul",
     "DEVERR_WAIT_OPERANDS", "DEVERR_WAIT_SLOT", "DEVERR_WAIT_ACCUM", "DEVERR_WAIT_DRAIN",
 ]
 
@@ -79,6 +79,7 @@ def load_library():
         "w8a8_linear": ([P, P, P, I, I, I, I, P, P, P, Z, P], S),
         "w8a8_add_rmsnorm_quantize": ([P, L, P, L, P, F, I, I, I, I, P, L, P, L, P, P], S),
         "w8a8_silu_mul_quantize": ([P, L, P, L, I, I, I, I, P, L, P, P], S),
+        "w8a8_matmul": ([P, L, P, P, L, P, I, I, I, I, P, I, P, L, P], S),
         "w4a8_quantize_weights": ([P, I, I, I, P, P, P, P], S),
         "w4a8_gemm": ([P, P, P, P, P, I, I, I, I, P, P, P, P], S),
         "w4a8_workspace_bytes": ([I, I], Z),
@@ -369,6 +370,32 @@ def w8a8_silu_mul_quantize(gate, up, group=0, Xq=None, x_scale=None, stream=None
         _check(fn, load_library().w8a8_silu_mul_quantize(
             a, lda, b, ldb, M, K, group, _dtype_code(dt), q, ldq, s, st))
     return Xq, x_scale
+
+
+def w8a8_matmul(Xq, x_scale, Wq, w_scale, group=0, bias=None, Y=None, dtype=None, stream=None):
+    """The int8 product with token and channel scales for any sizes: Y [M, N] =
+    ((Xq Wq^T * x_scale) * w_scale) / group + bias in bf16, fp16 or fp32 (the
+    type of Y, else `dtype`, else bf16; the bias is of the same type).  Code
+    matrices have rows a multiple of 16 bytes apart, Y rows of any stride."""
+    import torch
+    fn = "w8a8_matmul"
+    M, K = Xq.shape
+    N = Wq.shape[0]
+    dev = Xq.device
+    with _launch_on(dev, stream) as st:
+        a, lda = _matrix(fn, Xq, (M, K), torch.int8, dev)
+        b, ldb = _matrix(fn, Wq, (N, K), torch.int8, dev)
+        sa = _vector(fn, x_scale, M, torch.float32, dev)
+        sb = _vector(fn, w_scale, N, torch.float32, dev)
+        if Y is None:
+            Y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=dev)
+        dt = Y.dtype
+        _require(dtype is None or dtype == dt, fn, 1)
+        v = None if bias is None else _vector(fn, bias, N, dt, dev)
+        y, ldy = _matrix(fn, Y, (M, N), dt, dev)
+        _check(fn, load_library().w8a8_matmul(
+            a, lda, sa, b, ldb, sb, M, N, K, group, v, _dtype_code(dt), y, ldy, st))
+    return Y
 
 
 def w4a8_quantize_weights(W, group, Wq=None, w_scale=None, w_zero=None, stream=None):

@@ -394,6 +394,28 @@ w4a4_status w8a8_silu_mul_quantize(const void* gate, int64_t ldg, const void* up
   return cuda_status(launch_row_quantize(a, true, (int)dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+w4a4_status w8a8_matmul(const int8_t* Xq, int64_t ldx, const float* x_scale, const int8_t* Wq, int64_t ldw,
+                        const float* w_scale, int M, int N, int K, int group, const void* bias, w4a4_dtype dtype,
+                        void* Y, int64_t ldy, w4a4_stream_t stream) {
+  if (!dtype_ok(dtype)) return W4A4_ERR_INVALID_ARG;
+  // K: 128 * 128 * K stays inside an int32 accumulator
+  if (M < 0 || N < 1 || K < 1 || K > 131071) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  if (group != 0 && group != 64 && group != 128) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0) return W4A4_OK;
+  if (!Xq || !x_scale || !Wq || !w_scale || !Y) return W4A4_ERR_INVALID_ARG;
+  if (!code_rows_ok(M, ldx, K) || !code_rows_ok(N, ldw, K) || !stride_ok(M, ldy, N)) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  const size_t es = dtype_bytes(dtype);
+  if (!aligned16(Xq) || !aligned16(Wq) || !aligned_to(x_scale, 4) || !aligned_to(w_scale, 4) ||
+      !aligned_to(bias, es) || !aligned_to(Y, es))
+    return W4A4_ERR_MISALIGNED;
+  w4a4_status s = check_device();
+  if (s != W4A4_OK) return s;
+  const bool vec = aligned_to(Y, 4 * es) && (M == 1 || ldy % 4 == 0);
+  const float inv_group = group > 0 ? 1.0f / (float)group : 1.0f;
+  const Matmul8Args a{Xq, x_scale, Wq, w_scale, bias, Y, ldx, ldw, ldy, M, N, K, inv_group, vec};
+  return cuda_status(launch_matmul8(a, (int)dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 // ------------------------------------------------------------------ runtime LoRA
 w4a4_status w4a4_lora_merge(const void* L1, const void* L2, int rank, const void* A, const void* B, int lora_rank,
                             float lora_scale, int K, int N, void* L1_out, void* L2_out, w4a4_stream_t stream) {

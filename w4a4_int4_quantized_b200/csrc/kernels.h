@@ -82,4 +82,20 @@ struct RowQuantArgs {
 // dtype: 0 bf16, 1 fp16, 2 fp32
 cudaError_t launch_row_quantize(const RowQuantArgs& a, bool silu, int dtype, cudaStream_t st);
 
+// The int8 product for any sizes (csrc/matmul8.cu).  Strides count elements.
+struct Matmul8Args {
+  const int8_t* A;         // activation codes [M, K], rows lda apart (lda % 16 == 0)
+  const float* a_scale;    // [M]
+  const int8_t* B;         // weight codes [N, K], rows ldb apart (ldb % 16 == 0)
+  const float* b_scale;    // [N]
+  const void* bias;        // [N] of the output's type, or null
+  void* Y;                 // [M, N], rows ldy apart
+  int64_t lda, ldb, ldy;
+  int M, N, K;
+  float inv_group;
+  bool vec_out;            // four output elements at a multiple of four columns are aligned to their size
+};
+// dtype of Y and bias: 0 bf16, 1 fp16, 2 fp32
+cudaError_t launch_matmul8(const Matmul8Args& a, int dtype, cudaStream_t st);
+
 }  // namespace w4a4

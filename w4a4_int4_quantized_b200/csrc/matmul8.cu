@@ -1,0 +1,605 @@
+// int8 x int8 matrix product with a scale per token and per output channel,
+// for any M, N and K and strided rows:
+//   acc[m][n] = sum_k xq[m][k] wq[n][k]   (exact int32)
+//   Y[m][n]   = ((acc * s_x[m]) * s_w[n]) * (1 / g) + bias[n], rounded once to
+//               bf16, fp16 or fp32 (the epilogue order of the layers' GEMMs).
+//
+// Few tokens are bound by reading the weights once, many by the tensor cores,
+// so there are two kernels:
+//
+// few_tokens_kernel   a block owns 16 output channels, its warps split K.
+//   Weights go from global memory straight into the registers of mma.sync
+//   m16n8k32: a lane loads 16 consecutive codes of a channel and of a token
+//   and uses them as the fragments of two products; both operands see the
+//   same permutation of k, which the sum does not notice.  The warps' int32
+//   partials meet in shared memory.
+//
+// tile_kernel         a cluster of two CTAs owns a 256 x BN tile and issues
+//   tcgen05.mma kind::i8 in its pair form: each CTA holds 128 rows of A and
+//   BN / 2 of B per stage, 128 bytes of k wide in the 128-byte swizzle that
+//   TMA writes.  Two accumulators of BN columns in tensor memory let the
+//   epilogue of one tile run under the products of the next.  TMA fills what
+//   lies past M, N or K with zeros.
+//     warp 0       TMA loads (both CTAs; both complete on the even CTA's
+//                  barrier)
+//     warp 1       MMA issue (even CTA)
+//     warps 4-11   epilogue: tensor memory -> registers -> shared memory
+//                  (int32, 32 x 32 per warp) -> row-major registers, scales,
+//                  coalesced stores
+//   SPLIT: too few tiles for the GPU; a cluster of 2 S CTAs owns one tile, pair
+//   q takes a slice of K, and the int32 partials are summed exactly through
+//   distributed shared memory, rows interleaved over the pairs.
+// Every mbarrier wait is bounded; on timeout the kernel records an error in
+// the device error word and runs to completion.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "plan_cache.h"
+#include "tmap.h"
+
+namespace w4a4 {
+
+unsigned int* device_error_word();
+
+namespace {
+
+struct OutBf16 {
+  using elem = __nv_bfloat16;
+  static __device__ __forceinline__ elem from(float f) { return __float2bfloat16_rn(f); }
+  static __device__ __forceinline__ float to(elem e) { return __bfloat162float(e); }
+};
+struct OutFp16 {
+  using elem = __half;
+  static __device__ __forceinline__ elem from(float f) { return __float2half_rn(f); }
+  static __device__ __forceinline__ float to(elem e) { return __half2float(e); }
+};
+struct OutFp32 {
+  using elem = float;
+  static __device__ __forceinline__ elem from(float f) { return f; }
+  static __device__ __forceinline__ float to(elem e) { return e; }
+};
+
+__device__ __forceinline__ float dequant(int acc, float sx, float sw, float inv_group, float bias, bool has_bias) {
+  float y = __fmul_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw), inv_group);
+  return has_bias ? __fadd_rn(y, bias) : y;
+}
+
+// Four consecutive elements, n of them inside the row; vec: the address is
+// aligned to their size.
+template <class O>
+__device__ __forceinline__ void store4(typename O::elem* p, int n, bool vec, const float (&y)[4]) {
+  typename O::elem e[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) e[j] = O::from(y[j]);
+  if (vec && n >= 4) {
+    if constexpr (sizeof(typename O::elem) == 2) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(e);
+    else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(e);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) p[j] = e[j];
+  }
+}
+
+// ------------------------------------------------------------------ few tokens
+constexpr int kFewWarps = 8;
+constexpr int kFewRows = 16;     // output channels per block
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// 16 codes at k0 of a row of K codes (16-byte aligned): zeros past K, nothing
+// read there.
+template <bool STREAM>
+__device__ __forceinline__ uint4 load_codes(const int8_t* row, int k0, int K, bool in) {
+  if (!in || k0 >= K) return make_uint4(0u, 0u, 0u, 0u);
+  if (k0 + 16 <= K) return STREAM ? ldg_stream(row + k0) : __ldg(reinterpret_cast<const uint4*>(row + k0));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  for (int i = 0; i < K - k0; ++i) {
+    const uint32_t b = (uint32_t)(uint8_t)row[k0 + i] << (8 * (i & 3));
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j == i >> 2) w[j] |= b;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NB: blocks of 8 tokens.
+template <int NB, class O>
+__global__ void __launch_bounds__(kFewWarps * 32) few_tokens_kernel(Matmul8Args p) {
+  constexpr int U = NB <= 2 ? 4 : 2;      // k steps (64 codes) in flight per warp
+  __shared__ int part[kFewWarps][8 * NB][kFewRows + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int64_t n0 = (int64_t)blockIdx.x * kFewRows;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
+  const int8_t* w0 = p.B + (n0 + g) * p.ldb;
+  const int8_t* w1 = p.B + (n0 + g + 8) * p.ldb;
+  int acc[NB][4] = {};
+  const int steps = (p.K + 63) / 64;
+  for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
+    uint4 a[U][2], b[U][NB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
+      a[u][0] = load_codes<true>(w0, k0, p.K, in0);
+      a[u][1] = load_codes<true>(w1, k0, p.K, in1);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const int m = 8 * i + g;
+        b[u][i] = load_codes<false>(p.A + (int64_t)m * p.lda, k0, p.K, m < p.M);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        mma_s8(acc[i], a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u][i].x, b[u][i].y);
+        mma_s8(acc[i], a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u][i].z, b[u][i].w);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    part[warp][8 * i + 2 * t][g] = acc[i][0];
+    part[warp][8 * i + 2 * t + 1][g] = acc[i][1];
+    part[warp][8 * i + 2 * t][g + 8] = acc[i][2];
+    part[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 8 * NB * kFewRows; i += kFewWarps * 32) {
+    const int m = i / kFewRows, c = i % kFewRows;
+    const int64_t n = n0 + c;
+    if (m >= p.M || n >= p.N) continue;
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) sum += part[w][m][c];
+    const auto* bias = static_cast<const typename O::elem*>(p.bias);
+    const float y = dequant(sum, p.a_scale[m], p.b_scale[n], p.inv_group, bias ? O::to(bias[n]) : 0.0f, bias != nullptr);
+    static_cast<typename O::elem*>(p.Y)[(int64_t)m * p.ldy + n] = O::from(y);
+  }
+}
+
+// ------------------------------------------------------------------ tiles
+constexpr int BM = 128;              // A rows per CTA
+constexpr int BK = 128;              // codes per k-block: one swizzle row
+constexpr int kTileThreads = 384;
+constexpr int kEpiWarp0 = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kStagePitch = 32 * 4 + 16;                    // epilogue staging: row of 32 int32, bank-spread
+constexpr int kStageBytes = 32 * kStagePitch;               // per epilogue warp
+constexpr int kSmemLimit = 232448;
+
+template <int BN>
+struct TileCfg {
+  static constexpr int kBRows = BN / 2;
+  static constexpr int kABytes = BM * BK, kBBytes = kBRows * BK;
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kEpi = kEpiWarps * kStageBytes;
+  static constexpr int kBarBytes = 512;
+  static constexpr int ST = (kSmemLimit - 1024 - kEpi - kBarBytes) / kStage;
+  static constexpr int kRing = ST * kStage;
+  static constexpr int kSmem = 1024 + kRing + kEpi + kBarBytes;
+  static constexpr int kPartPitch = BN * 4 + 16;            // split: int32 partial row, bank-spread
+  static constexpr int kTmemCols = 2 * BN;
+  static_assert(ST >= 4 && ST <= 12, "ring depth");
+  static_assert(BM * kPartPitch <= kRing + kEpi, "partials fit where the ring was");
+  static_assert(kSmem <= kSmemLimit, "shared memory budget");
+};
+
+struct TileBars {
+  uint64_t full[12], empty[12], acc_full[2], acc_empty[2];
+  uint32_t tmem_base;
+};
+static_assert(sizeof(TileBars) <= 512, "barrier area");
+
+// TMA load whose bytes complete on a barrier of either CTA of the pair (a
+// shared::cluster address).  No multicast.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+struct TilePlan {
+  int tiles_m, tiles_n, split;
+};
+
+// Tile t of a walk that goes down up to eight row tiles before it moves one
+// column tile on, so that the pairs at work together share their operands in L2.
+__device__ __forceinline__ void tile_at(int64_t t, const TilePlan& pl, int& tm, int& tn) {
+  const int64_t per = (int64_t)8 * pl.tiles_n;
+  const int band = (int)(t / per);
+  const int rows = min(8, pl.tiles_m - 8 * band);
+  const int64_t in = t - band * per;
+  tn = (int)(in / rows);
+  tm = 8 * band + (int)(in - (int64_t)tn * rows);
+}
+
+template <int BN, class O, bool SPLIT>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    tile_kernel(const Matmul8Args p, const TilePlan pl, const __grid_constant__ CUtensorMap tmA,
+                const __grid_constant__ CUtensorMap tmB, unsigned int* err) {
+  using C = TileCfg<BN>;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* gbase = raw + (base - smem_u32(raw));
+  TileBars* bar = reinterpret_cast<TileBars*>(gbase + C::kRing + C::kEpi);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t half = crank & 1u;                  // 0: the pair's even CTA
+  const uint32_t lead = crank & ~1u;
+  const uint16_t pmask = (uint16_t)(3u << lead);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(&bar->full[s], 1);
+      mbar_init(&bar->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bar->acc_full[b], 1);
+      mbar_init(&bar->acc_empty[b], 2 * kEpiWarps);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(&bar->tmem_base, C::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  grid_dependency_wait();
+
+  // This pair's tiles and k-blocks.
+  const int64_t tiles = (int64_t)pl.tiles_m * pl.tiles_n;
+  const int nk = (p.K + BK - 1) / BK;
+  int64_t t0, tstep;
+  int kb0 = 0, kb1 = nk;
+  if constexpr (SPLIT) {
+    t0 = blockIdx.x / (2 * pl.split);
+    tstep = tiles;                                   // one tile
+    const int q = (int)(crank >> 1);
+    kb0 = (int)((int64_t)q * nk / pl.split);
+    kb1 = (int)((int64_t)(q + 1) * nk / pl.split);
+  } else {
+    t0 = blockIdx.x >> 1;
+    tstep = gridDim.x >> 1;
+  }
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA
+    if (lane == 0) {
+      int g = 0;
+      bool ok = true;
+      for (int64_t t = t0; t < tiles && ok; t += tstep) {
+        int tm, tn;
+        tile_at(t, pl, tm, tn);
+        const int ya = tm * 2 * BM + (int)half * BM, yb = tn * BN + (int)half * C::kBRows;
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
+          const int s = g % C::ST;
+          if (g >= C::ST && !mbar_wait_cluster(&bar->empty[s], (uint32_t)(g / C::ST - 1) & 1u)) {
+            set_device_error(err, kDevErrTimeoutEmpty);
+            ok = false;
+            break;
+          }
+          if (half == 0) mbar_arrive_expect_tx(&bar->full[s], 2u * (uint32_t)C::kStage);
+          const uint32_t fb = map_to_rank(smem_u32(&bar->full[s]), lead);
+          const uint32_t dst = base + (uint32_t)(s * C::kStage);
+          tma_load_2d_pair(dst, &tmA, kb * BK, ya, fb);
+          tma_load_2d_pair(dst + C::kABytes, &tmB, kb * BK, yb, fb);
+        }
+      }
+      // every stage given back: no copy, product or arrival is in flight
+      // towards this CTA any more
+      for (int s = 0; s < C::ST && ok; ++s) {
+        const int uses = (g - s + C::ST - 1) / C::ST;
+        if (uses > 0 && !mbar_wait_cluster(&bar->empty[s], (uint32_t)(uses - 1) & 1u)) {
+          set_device_error(err, kDevErrTimeoutDrain);
+          ok = false;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && half == 0) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_i8(2 * BM, BN);
+      int g = 0, i = 0;
+      bool ok = true;
+      for (int64_t t = t0; t < tiles && ok; t += tstep, ++i) {
+        const int b = i & 1;
+        if (i >= 2 && !mbar_wait_cluster(&bar->acc_empty[b], (uint32_t)(i / 2 - 1) & 1u)) {
+          set_device_error(err, kDevErrTimeoutAcc);
+          break;
+        }
+        tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
+          const int s = g % C::ST;
+          if (!mbar_wait_cluster(&bar->full[s], (uint32_t)(g / C::ST) & 1u)) {
+            set_device_error(err, kDevErrTimeoutFull);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = base + (uint32_t)(s * C::kStage);
+#pragma unroll
+          for (int ks = 0; ks < BK / 32; ++ks)
+            mma_i8_ss_pair(tmem + (uint32_t)(b * BN), smem_desc_kmajor_sw128(st + (uint32_t)(ks * 32)),
+                           smem_desc_kmajor_sw128(st + C::kABytes + (uint32_t)(ks * 32)), idesc,
+                           kb > kb0 || ks > 0 ? 1u : 0u);
+          tc_commit_pair_mc(&bar->empty[s], pmask);
+        }
+        if (ok) tc_commit_pair_mc(&bar->acc_full[b], pmask);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kEpiWarp0) {
+    // ---------------------------------------------------------------- epilogue
+    const int ew = warp - kEpiWarp0;
+    const int quad = warp & 3, hc = ew >> 2;
+    constexpr int kCols = BN / 2;                    // columns of a warp
+    if constexpr (SPLIT) {
+      if (mbar_wait_cluster(&bar->acc_full[0], 0u)) {
+        tc_fence_after();
+        const uint32_t row = base + (uint32_t)((quad * 32 + lane) * C::kPartPitch + hc * kCols * 4);
+#pragma unroll
+        for (int ch = 0; ch < kCols / 32; ++ch) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(hc * kCols + ch * 32), v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + (uint32_t)(ch * 128 + j * 16)),
+                         "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3])
+                         : "memory");
+        }
+      } else {
+        set_device_error(err, kDevErrTimeoutAcc);
+      }
+    } else {
+      const uint32_t stg = base + (uint32_t)(C::kRing + ew * kStageBytes);
+      const int cl = (lane & 7) * 4, rl = lane >> 3;  // this lane's columns and first row when rows are read back
+      int i = 0;
+      for (int64_t t = t0; t < tiles; t += tstep, ++i) {
+        const int b = i & 1;
+        int tm, tn;
+        tile_at(t, pl, tm, tn);
+        const int64_t m0 = (int64_t)tm * 2 * BM + (int64_t)half * BM + quad * 32;
+        const int64_t n0 = (int64_t)tn * BN + hc * kCols + cl;
+        const float sx = m0 + lane < p.M ? p.a_scale[m0 + lane] : 0.0f;
+        float sw[kCols / 32][4], bs[kCols / 32][4];
+#pragma unroll
+        for (int ch = 0; ch < kCols / 32; ++ch)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t n = n0 + ch * 32 + j;
+            const auto* bias = static_cast<const typename O::elem*>(p.bias);
+            sw[ch][j] = n < p.N ? p.b_scale[n] : 0.0f;
+            bs[ch][j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
+          }
+        if (!mbar_wait_cluster(&bar->acc_full[b], (uint32_t)(i / 2) & 1u)) {
+          set_device_error(err, kDevErrTimeoutAcc);
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int ch = 0; ch < kCols / 32; ++ch) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BN + hc * kCols + ch * 32), v);
+          tmem_wait_ld();
+          if (ch == kCols / 32 - 1) {                 // the accumulator may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(&bar->acc_empty[b], lead);
+          }
+          __syncwarp();                               // the last chunk's rows are read
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stg + (uint32_t)(lane * kStagePitch + j * 16)),
+                         "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3])
+                         : "memory");
+          __syncwarp();
+          const int64_t n = n0 + ch * 32;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int row = r * 4 + rl;
+            uint4 a;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w)
+                         : "r"(stg + (uint32_t)(row * kStagePitch + cl * 4)));
+            const float s = __shfl_sync(0xFFFFFFFFu, sx, row);
+            const int64_t m = m0 + row;
+            if (m < p.M && n < p.N) {
+              const bool hb = p.bias != nullptr;
+              const float y[4] = {dequant((int)a.x, s, sw[ch][0], p.inv_group, bs[ch][0], hb),
+                                  dequant((int)a.y, s, sw[ch][1], p.inv_group, bs[ch][1], hb),
+                                  dequant((int)a.z, s, sw[ch][2], p.inv_group, bs[ch][2], hb),
+                                  dequant((int)a.w, s, sw[ch][3], p.inv_group, bs[ch][3], hb)};
+              store4<O>(static_cast<typename O::elem*>(p.Y) + m * p.ldy + n, (int)min((int64_t)4, p.N - n),
+                        p.vec_out, y);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if constexpr (SPLIT) {
+    // Rows r = q, q + S, ... of this CTA's 128: the pairs' partials summed, a
+    // lane per four columns.
+    constexpr int kG = BN / 128;                     // groups of four columns per lane
+    int tm, tn;
+    tile_at(t0, pl, tm, tn);
+    const int64_t m0 = (int64_t)tm * 2 * BM + (int64_t)half * BM;
+    const int64_t n0 = (int64_t)tn * BN + lane * 4;
+    const int S = pl.split;
+    float sw[kG][4], bs[kG][4];
+#pragma unroll
+    for (int c = 0; c < kG; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t n = n0 + c * 128 + j;
+        const auto* bias = static_cast<const typename O::elem*>(p.bias);
+        sw[c][j] = n < p.N ? p.b_scale[n] : 0.0f;
+        bs[c][j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
+      }
+    uint32_t peer[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) peer[q] = map_to_rank(base, (uint32_t)(2 * (q < S ? q : 0)) + half);
+    for (int r = (int)(crank >> 1) + warp * S; r < BM; r += (kTileThreads / 32) * S) {
+      const int64_t m = m0 + r;
+      if (m >= p.M) break;
+      const float s = p.a_scale[m];
+      uint4 v[4][kG];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int c = 0; c < kG; ++c)
+          if (q < S) v[q][c] = ld_cluster_v4(peer[q] + (uint32_t)(r * C::kPartPitch + (c * 128 + lane * 4) * 4));
+#pragma unroll
+      for (int c = 0; c < kG; ++c) {
+        int a[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < S) {
+            a[0] += (int)v[q][c].x;
+            a[1] += (int)v[q][c].y;
+            a[2] += (int)v[q][c].z;
+            a[3] += (int)v[q][c].w;
+          }
+        const int64_t n = n0 + c * 128;
+        if (n >= p.N) continue;
+        const bool hb = p.bias != nullptr;
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], s, sw[c][j], p.inv_group, bs[c][j], hb);
+        store4<O>(static_cast<typename O::elem*>(p.Y) + m * p.ldy + n, (int)min((int64_t)4, p.N - n), p.vec_out, y);
+      }
+    }
+    cluster_sync();                                  // the partials stay readable until every CTA has summed
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+template <int NB, class O>
+cudaError_t launch_few(const Matmul8Args& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.N + kFewRows - 1) / kFewRows), 1, 1);
+  cfg.blockDim = dim3(kFewWarps * 32, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<NB, O>, a);
+}
+
+template <int BN, class O, bool SPLIT>
+cudaError_t launch_tile(const Matmul8Args& a, const TilePlan& pl, int sms, int dev, cudaStream_t st) {
+  using C = TileCfg<BN>;
+  auto kern = tile_kernel<BN, O, SPLIT>;
+  static DeviceFlags configured;
+  cudaError_t e;
+  if (!configured.done(dev)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess)
+      return e;
+    configured.set(dev);
+  }
+  unsigned int* err = device_error_word();
+  if (!err) return cudaErrorInvalidDevicePointer;
+  CUtensorMap tA, tB;
+  auto codes = [&](CUtensorMap* tm, const int8_t* x, int rows, int64_t ld, int box) {
+    const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)rows};
+    const uint64_t strides[1] = {(uint64_t)(rows == 1 ? (a.K + 15) / 16 * 16 : ld)};
+    const uint32_t bx[2] = {BK, (uint32_t)box};
+    return make_tmap_nd(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, 2, dims, strides, bx, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!codes(&tA, a.A, a.M, a.lda, BM) || !codes(&tB, a.B, a.N, a.ldb, C::kBRows)) return cudaErrorInvalidValue;
+  const int64_t tiles = (int64_t)pl.tiles_m * pl.tiles_n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(SPLIT ? 2 * pl.split * tiles : 2 * std::min<int64_t>(tiles, sms / 2)), 1, 1);
+  cfg.blockDim = dim3(kTileThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = SPLIT ? 2 * pl.split : 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, pl, tA, tB, err);
+}
+
+template <class O>
+cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
+  if (a.M <= 8) return launch_few<1, O>(a, st);
+  if (a.M <= 16) return launch_few<2, O>(a, st);
+  if (a.M <= 32) return launch_few<4, O>(a, st);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
+  const int tiles_m = (a.M + 2 * BM - 1) / (2 * BM);
+  const int nk = (a.K + BK - 1) / BK;
+  const int n256 = (a.N + 255) / 256, n128 = (a.N + 127) / 128;
+  for (int s : {4, 2}) {
+    if (nk < 2 * s) continue;
+    if ((int64_t)tiles_m * n256 * s * 2 <= sms * 9 / 10 && (int64_t)tiles_m * n128 * s * 2 > sms * 9 / 10)
+      return launch_tile<256, O, true>(a, TilePlan{tiles_m, n256, s}, sms, dev, st);
+    if ((int64_t)tiles_m * n128 * s * 2 <= sms * 9 / 10)
+      return launch_tile<128, O, true>(a, TilePlan{tiles_m, n128, s}, sms, dev, st);
+  }
+  if ((int64_t)tiles_m * n128 * 2 <= sms) return launch_tile<128, O, false>(a, TilePlan{tiles_m, n128, 1}, sms, dev, st);
+  return launch_tile<256, O, false>(a, TilePlan{tiles_m, n256, 1}, sms, dev, st);
+}
+
+}  // namespace
+
+cudaError_t launch_matmul8(const Matmul8Args& a, int dtype, cudaStream_t st) {
+  if (dtype == 0) return launch_out<OutBf16>(a, st);
+  if (dtype == 1) return launch_out<OutFp16>(a, st);
+  return launch_out<OutFp32>(a, st);
+}
+
+}  // namespace w4a4
