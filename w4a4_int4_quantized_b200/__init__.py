@@ -257,72 +257,92 @@ def w8a8_linear(X, Wq, w_scale, group, bias=None, Y=None, workspace=None, stream
 
 
 # ---- around the INT8 product: strided rows, three element types -------------
+#
+# A decoded token's kernels take 2 to 6 us, so what these functions do before
+# the launch is kept short: the common case (tensors of the current device, its
+# current stream) goes straight to the C call, with no context managers and
+# the raw stream handle.
 
-_DTYPES = None          # torch dtype -> W4A4_DTYPE_*, filled on first use
-
-
-def _dtype_code(dtype):
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    return _DTYPES.get(dtype, -1)      # -1: the library answers W4A4_ERR_INVALID_ARG
+_torch = _dtypes = _raw_stream = _cur_device = None
 
 
-def _require(ok, fn, status):
-    if not ok:
-        raise W4A4Error(fn, status)
+def _bind_torch():
+    global _torch, _dtypes, _raw_stream, _cur_device
+    import torch
+    load_library()
+    _dtypes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    _raw_stream, _cur_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _torch = torch
 
 
-def _matrix(fn, t, shape, dtype, device):
+def _matrix(fn, t, shape, dtype, dev):
     """Data pointer and row stride (in elements) of a matrix whose rows are
-    contiguous; refuses another shape, element type or device."""
-    _require(t.dtype == dtype and t.device == device, fn, 1)
-    _require(t.shape == shape, fn, 2)
-    rows, cols = t.stride()
-    _require(cols == 1 or shape[1] == 1, fn, 2)
-    return t.data_ptr(), rows
+    contiguous; refuses another shape (M, K), element type or device."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise W4A4Error(fn, 1)
+    if t.shape != shape:
+        raise W4A4Error(fn, 2)
+    ld, one = t.stride()
+    if one != 1 and shape[1] != 1:
+        raise W4A4Error(fn, 2)
+    return t.data_ptr(), ld
 
 
-def _vector(fn, t, n, dtype, device):
-    _require(t.dtype == dtype and t.device == device, fn, 1)
-    _require(t.shape == (n,) and (n <= 1 or t.stride(0) == 1), fn, 2)
+def _vector(fn, t, n, dtype, dev):
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise W4A4Error(fn, 1)
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise W4A4Error(fn, 2)
     return t.data_ptr()
 
 
-class _launch_on:
-    """The raw stream to launch on, with its device current and (for a stream
-    that was given) outputs allocated on it."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guard = None
-        if device.type != "cuda":
-            raise W4A4Error("stream", 6)
-        if stream is not None:
-            self.guard = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        import torch
-        if self.guard is not None:
-            self.guard.__enter__()
-        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _codes_out(M, K, like):
+    """A code matrix [M, K] with rows 16-byte aligned."""
+    return _torch.empty((M, (K + 15) // 16 * 16), dtype=_torch.int8, device=like.device)[:, :K]
 
 
-def _codes_out(fn, Xq, M, K, device):
-    """A code matrix [M, K] with rows 16-byte aligned: (tensor, pointer, stride)."""
-    import torch
+def _run(fn, core, dev, stream, *args):
+    """core(*args, dev, raw stream) with the tensors' device current; outputs
+    that core allocates belong to the stream that it launches on."""
+    if dev < 0:
+        raise W4A4Error(fn, 6)
+    if stream is None:
+        if dev == _cur_device():
+            return core(*args, dev, _raw_stream(dev))
+        with _torch.cuda.device(dev):
+            return core(*args, dev, _raw_stream(dev))
+    if stream.device.index != dev:
+        raise W4A4Error(fn, 1)
+    with _torch.cuda.stream(stream):
+        return core(*args, dev, stream.cuda_stream)
+
+
+def _add_rmsnorm_quantize(X, gamma, eps, group, residual, H, Xq, x_scale, dev, st):
+    fn = "w8a8_add_rmsnorm_quantize"
+    dt = X.dtype
+    shape = M, K = X.shape
+    x, ldx = _matrix(fn, X, shape, dt, dev)
+    r = g = h = None
+    ldr = ldh = 0
+    if residual is not None:
+        r, ldr = _matrix(fn, residual, shape, dt, dev)
+        if H is None:
+            H = _torch.empty((M, K), dtype=dt, device=X.device)
+    if gamma is not None:
+        g = _vector(fn, gamma, K, dt, dev)
+    if H is not None:
+        h, ldh = _matrix(fn, H, shape, dt, dev)
     if Xq is None:
-        Xq = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
-    q, ldq = _matrix(fn, Xq, (M, K), torch.int8, device)
-    return Xq, q, ldq
+        Xq = _codes_out(M, K, X)
+    if x_scale is None:
+        x_scale = _torch.empty((M,), dtype=_torch.float32, device=X.device)
+    q, ldq = _matrix(fn, Xq, shape, _torch.int8, dev)
+    s = _vector(fn, x_scale, M, _torch.float32, dev)
+    status = _lib.w8a8_add_rmsnorm_quantize(x, ldx, r, ldr, g, eps, M, K, group, _dtypes.get(dt, -1), h, ldh, q, ldq,
+                                            s, st)
+    if status:
+        raise W4A4Error(fn, status)
+    return Xq, x_scale, H
 
 
 def w8a8_add_rmsnorm_quantize(X, gamma, eps, group=0, residual=None, H=None, Xq=None, x_scale=None, stream=None):
@@ -332,44 +352,58 @@ def w8a8_add_rmsnorm_quantize(X, gamma, eps, group=0, residual=None, H=None, Xq=
     (X + residual rounded to the type) is allocated when there is a residual
     and None otherwise; it may be X or residual itself.  Codes allocated here
     have their rows 16-byte aligned (a stride of K rounded up)."""
-    import torch
-    fn = "w8a8_add_rmsnorm_quantize"
-    M, K = X.shape
-    dt, dev = X.dtype, X.device
-    with _launch_on(dev, stream) as st:
-        x, ldx = _matrix(fn, X, (M, K), dt, dev)
-        r, ldr = (None, 0) if residual is None else _matrix(fn, residual, (M, K), dt, dev)
-        g = None if gamma is None else _vector(fn, gamma, K, dt, dev)
-        if H is None and residual is not None:
-            H = torch.empty((M, K), dtype=dt, device=dev)
-        h, ldh = (None, 0) if H is None else _matrix(fn, H, (M, K), dt, dev)
-        Xq, q, ldq = _codes_out(fn, Xq, M, K, dev)
-        if x_scale is None:
-            x_scale = torch.empty((M,), dtype=torch.float32, device=dev)
-        s = _vector(fn, x_scale, M, torch.float32, dev)
-        _check(fn, load_library().w8a8_add_rmsnorm_quantize(
-            x, ldx, r, ldr, g, eps, M, K, group, _dtype_code(dt), h, ldh, q, ldq, s, st))
-    return Xq, x_scale, H
+    if _torch is None:
+        _bind_torch()
+    return _run("w8a8_add_rmsnorm_quantize", _add_rmsnorm_quantize, X.get_device(), stream, X, gamma, eps, group,
+                residual, H, Xq, x_scale)
+
+
+def _silu_mul_quantize(gate, up, group, Xq, x_scale, dev, st):
+    fn = "w8a8_silu_mul_quantize"
+    dt = gate.dtype
+    shape = M, K = gate.shape
+    a, lda = _matrix(fn, gate, shape, dt, dev)
+    b, ldb = _matrix(fn, up, shape, dt, dev)
+    if Xq is None:
+        Xq = _codes_out(M, K, gate)
+    if x_scale is None:
+        x_scale = _torch.empty((M,), dtype=_torch.float32, device=gate.device)
+    q, ldq = _matrix(fn, Xq, shape, _torch.int8, dev)
+    s = _vector(fn, x_scale, M, _torch.float32, dev)
+    status = _lib.w8a8_silu_mul_quantize(a, lda, b, ldb, M, K, group, _dtypes.get(dt, -1), q, ldq, s, st)
+    if status:
+        raise W4A4Error(fn, status)
+    return Xq, x_scale
 
 
 def w8a8_silu_mul_quantize(gate, up, group=0, Xq=None, x_scale=None, stream=None):
     """SiLU(gate) * up, rotation and per-token int8 quantization in one kernel:
     (codes [M, K], scales [M]).  gate and up are bf16, fp16 or fp32 [M, K],
     rows of any stride: the halves of one [M, 2 K] product need no copy."""
-    import torch
-    fn = "w8a8_silu_mul_quantize"
-    M, K = gate.shape
-    dt, dev = gate.dtype, gate.device
-    with _launch_on(dev, stream) as st:
-        a, lda = _matrix(fn, gate, (M, K), dt, dev)
-        b, ldb = _matrix(fn, up, (M, K), dt, dev)
-        Xq, q, ldq = _codes_out(fn, Xq, M, K, dev)
-        if x_scale is None:
-            x_scale = torch.empty((M,), dtype=torch.float32, device=dev)
-        s = _vector(fn, x_scale, M, torch.float32, dev)
-        _check(fn, load_library().w8a8_silu_mul_quantize(
-            a, lda, b, ldb, M, K, group, _dtype_code(dt), q, ldq, s, st))
-    return Xq, x_scale
+    if _torch is None:
+        _bind_torch()
+    return _run("w8a8_silu_mul_quantize", _silu_mul_quantize, gate.get_device(), stream, gate, up, group, Xq, x_scale)
+
+
+def _matmul8(Xq, x_scale, Wq, w_scale, group, bias, Y, dtype, dev, st):
+    fn = "w8a8_matmul"
+    M, K = Xq.shape
+    N = Wq.shape[0]
+    i8, f32 = _torch.int8, _torch.float32
+    a, lda = _matrix(fn, Xq, (M, K), i8, dev)
+    b, ldb = _matrix(fn, Wq, (N, K), i8, dev)
+    sa, sb = _vector(fn, x_scale, M, f32, dev), _vector(fn, w_scale, N, f32, dev)
+    if Y is None:
+        Y = _torch.empty((M, N), dtype=dtype or _torch.bfloat16, device=Xq.device)
+    dt = Y.dtype
+    if dtype is not None and dtype is not dt:
+        raise W4A4Error(fn, 1)
+    v = None if bias is None else _vector(fn, bias, N, dt, dev)
+    y, ldy = _matrix(fn, Y, (M, N), dt, dev)
+    status = _lib.w8a8_matmul(a, lda, sa, b, ldb, sb, M, N, K, group, v, _dtypes.get(dt, -1), y, ldy, st)
+    if status:
+        raise W4A4Error(fn, status)
+    return Y
 
 
 def w8a8_matmul(Xq, x_scale, Wq, w_scale, group=0, bias=None, Y=None, dtype=None, stream=None):
@@ -377,25 +411,9 @@ def w8a8_matmul(Xq, x_scale, Wq, w_scale, group=0, bias=None, Y=None, dtype=None
     ((Xq Wq^T * x_scale) * w_scale) / group + bias in bf16, fp16 or fp32 (the
     type of Y, else `dtype`, else bf16; the bias is of the same type).  Code
     matrices have rows a multiple of 16 bytes apart, Y rows of any stride."""
-    import torch
-    fn = "w8a8_matmul"
-    M, K = Xq.shape
-    N = Wq.shape[0]
-    dev = Xq.device
-    with _launch_on(dev, stream) as st:
-        a, lda = _matrix(fn, Xq, (M, K), torch.int8, dev)
-        b, ldb = _matrix(fn, Wq, (N, K), torch.int8, dev)
-        sa = _vector(fn, x_scale, M, torch.float32, dev)
-        sb = _vector(fn, w_scale, N, torch.float32, dev)
-        if Y is None:
-            Y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=dev)
-        dt = Y.dtype
-        _require(dtype is None or dtype == dt, fn, 1)
-        v = None if bias is None else _vector(fn, bias, N, dt, dev)
-        y, ldy = _matrix(fn, Y, (M, N), dt, dev)
-        _check(fn, load_library().w8a8_matmul(
-            a, lda, sa, b, ldb, sb, M, N, K, group, v, _dtype_code(dt), y, ldy, st))
-    return Y
+    if _torch is None:
+        _bind_torch()
+    return _run("w8a8_matmul", _matmul8, Xq.get_device(), stream, Xq, x_scale, Wq, w_scale, group, bias, Y, dtype)
 
 
 def w4a8_quantize_weights(W, group, Wq=None, w_scale=None, w_zero=None, stream=None):

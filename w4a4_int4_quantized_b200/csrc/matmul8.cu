@@ -5,14 +5,22 @@
 //               bf16, fp16 or fp32 (the epilogue order of the layers' GEMMs).
 //
 // Few tokens are bound by reading the weights once, many by the tensor cores,
-// so there are two kernels:
+// so there are three kernels:
 //
-// few_tokens_kernel   a block owns 16 output channels, its warps split K.
-//   Weights go from global memory straight into the registers of mma.sync
-//   m16n8k32: a lane loads 16 consecutive codes of a channel and of a token
-//   and uses them as the fragments of two products; both operands see the
-//   same permutation of k, which the sum does not notice.  The warps' int32
-//   partials meet in shared memory.
+// few_tokens_kernel   up to 8 tokens and small weights: a block owns 16 output
+//   channels, its warps split K.  Weights go from global memory straight into
+//   the registers of mma.sync m16n8k32: a lane loads 16 consecutive codes of a
+//   channel and of a token and uses them as the fragments of two products; both
+//   operands see the same permutation of k, which the sum does not notice.  The
+//   warps' int32 partials meet in shared memory.
+//
+// stream_kernel       up to 128 tokens: the weights are the 128-row operand of
+//   tcgen05.mma kind::i8 (one CTA), the tokens its N.  Both come by TMA through a
+//   ring of 108 KB, two CTAs per SM, so that the weights stream without a pause
+//   from tile to tile.  With few tiles K is split over a cluster and the int32
+//   partials are summed through distributed shared memory.  A stage costs about
+//   180 ns of TMA delivery (100 to 110 bytes per ns and SM) plus 23 ns per
+//   product, in which the operands' shared-memory reads hold the copies up.
 //
 // tile_kernel         a cluster of two CTAs owns a 256 x BN tile and issues
 //   tcgen05.mma kind::i8 in its pair form: each CTA holds 128 rows of A and
@@ -23,6 +31,7 @@
 //     warp 0       TMA loads (both CTAs; both complete on the even CTA's
 //                  barrier)
 //     warp 1       MMA issue (even CTA)
+//     warp 3       polls the barriers that the MMA warp depends on
 //     warps 4-11   epilogue: tensor memory -> registers -> shared memory
 //                  (int32, 32 x 32 per warp) -> row-major registers, scales,
 //                  coalesced stores
@@ -36,6 +45,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -123,23 +133,35 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// NB: blocks of 8 tokens.
-template <int NB, class O>
+// At most 8 tokens.  Bound by the latency of one round of loads: each warp has
+// all of U * kFewWarps * 64 = 4096 codes of k in flight at once, and the
+// weights are asked into L2 before the wait for the previous kernel (a hint;
+// the loads after the wait read memory as it then is).  N = K = 4096, one
+// token, replayed back to back: 6.1 us with U = 4, 6.1 with U = 8, 5.1 with
+// the hint and U = 8 (5.6 with U = 4).
+template <class O>
 __global__ void __launch_bounds__(kFewWarps * 32) few_tokens_kernel(Matmul8Args p) {
-  constexpr int U = NB <= 2 ? 4 : 2;      // k steps (64 codes) in flight per warp
-  __shared__ int part[kFewWarps][8 * NB][kFewRows + 1];
+  constexpr int U = 8;             // k steps (64 codes) in flight per warp
+  __shared__ int part[kFewWarps][8][kFewRows + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int64_t n0 = (int64_t)blockIdx.x * kFewRows;
+  {
+    const int64_t n = n0 + (threadIdx.x & (kFewRows - 1));
+    if (n < p.N)
+      for (int k = (threadIdx.x / kFewRows) * 128; k < p.K; k += kFewWarps * 32 / kFewRows * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.B + n * p.ldb + k));
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
+  const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N, inx = g < p.M;
   const int8_t* w0 = p.B + (n0 + g) * p.ldb;
   const int8_t* w1 = p.B + (n0 + g + 8) * p.ldb;
-  int acc[NB][4] = {};
+  const int8_t* x = p.A + (int64_t)g * p.lda;
+  int acc[4] = {};
   const int steps = (p.K + 63) / 64;
   for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
-    uint4 a[U][2], b[U][NB];
+    uint4 a[U][2], b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
@@ -147,34 +169,21 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_tokens_kernel(Matmul8Args 
       a[u][1] = load_codes<true>(w1, k0, p.K, in1);
     }
 #pragma unroll
+    for (int u = 0; u < U; ++u) b[u] = load_codes<false>(x, (s0 + u * kFewWarps) * 64 + 16 * t, p.K, inx);
+#pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        const int m = 8 * i + g;
-        b[u][i] = load_codes<false>(p.A + (int64_t)m * p.lda, k0, p.K, m < p.M);
-      }
+      mma_s8(acc, a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u].x, b[u].y);
+      mma_s8(acc, a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u].z, b[u].w);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        mma_s8(acc[i], a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u][i].x, b[u][i].y);
-        mma_s8(acc[i], a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u][i].z, b[u][i].w);
-      }
   }
-#pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    part[warp][8 * i + 2 * t][g] = acc[i][0];
-    part[warp][8 * i + 2 * t + 1][g] = acc[i][1];
-    part[warp][8 * i + 2 * t][g + 8] = acc[i][2];
-    part[warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
-  }
+  part[warp][2 * t][g] = acc[0];
+  part[warp][2 * t + 1][g] = acc[1];
+  part[warp][2 * t][g + 8] = acc[2];
+  part[warp][2 * t + 1][g + 8] = acc[3];
   __syncthreads();
-  for (int i = threadIdx.x; i < 8 * NB * kFewRows; i += kFewWarps * 32) {
-    const int m = i / kFewRows, c = i % kFewRows;
-    const int64_t n = n0 + c;
-    if (m >= p.M || n >= p.N) continue;
+  const int m = threadIdx.x / kFewRows, c = threadIdx.x % kFewRows;
+  const int64_t n = n0 + c;
+  if (m < p.M && m < 8 && n < p.N) {
     int sum = 0;
 #pragma unroll
     for (int w = 0; w < kFewWarps; ++w) sum += part[w][m][c];
@@ -190,6 +199,7 @@ constexpr int BK = 128;              // codes per k-block: one swizzle row
 constexpr int kTileThreads = 384;
 constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
+constexpr int kIssueBar = 1;             // named barrier: MMA warp + the warp that waits for it
 constexpr int kStagePitch = 32 * 4 + 16;                    // epilogue staging: row of 32 int32, bank-spread
 constexpr int kStageBytes = 32 * kStagePitch;               // per epilogue warp
 constexpr int kSmemLimit = 232448;
@@ -206,6 +216,10 @@ struct TileCfg {
   static constexpr int kSmem = 1024 + kRing + kEpi + kBarBytes;
   static constexpr int kPartPitch = BN * 4 + 16;            // split: int32 partial row, bank-spread
   static constexpr int kTmemCols = 2 * BN;
+  // k-blocks released to the MMA warp at a time: two narrow ones (256 x 128 x
+  // 8192 alone: 290 -> 250 ns each), one wide one (its four products cover the
+  // hand-off)
+  static constexpr int kBatch = BN == 128 ? 2 : 1;
   static_assert(ST >= 4 && ST <= 12, "ring depth");
   static_assert(BM * kPartPitch <= kRing + kEpi, "partials fit where the ring was");
   static_assert(kSmem <= kSmemLimit, "shared memory budget");
@@ -332,37 +346,66 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncwarp();
   } else if (warp == 1 && half == 0) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_i8(2 * BM, BN);
-      int g = 0, i = 0;
-      bool ok = true;
-      for (int64_t t = t0; t < tiles && ok; t += tstep, ++i) {
-        const int b = i & 1;
-        if (i >= 2 && !mbar_wait_cluster(&bar->acc_empty[b], (uint32_t)(i / 2 - 1) & 1u)) {
-          set_device_error(err, kDevErrTimeoutAcc);
-          break;
+    // This warp never reads shared memory: a read whose result it uses would
+    // queue behind the products it has issued.  Warp 3 polls the barriers in
+    // the same order and releases each step through a named barrier.
+    constexpr uint32_t idesc = idesc_i8(2 * BM, BN);
+    const uint64_t da0 = smem_desc_kmajor_sw128(base), db0 = smem_desc_kmajor_sw128(base + C::kABytes);
+    int s = 0, i = 0;
+    for (int64_t t = t0; t < tiles; t += tstep, ++i) {
+      const int b = i & 1;
+      bool bad = false;
+      for (int kb = kb0; kb < kb1;) {
+        if ((bad = named_barrier_or(kIssueBar, 64, false))) break;
+        if (kb == kb0) tc_fence_after();               // the epilogue has read this accumulator
+        const int end = min(kb + C::kBatch, kb1);
+        for (; kb < end; ++kb) {
+          if (lane == 0) {
+            const uint64_t off = (uint64_t)(s * (C::kStage >> 4));   // descriptors count 16 bytes
+#pragma unroll
+            for (int ks = 0; ks < BK / 32; ++ks)
+              mma_i8_ss_pair(tmem + (uint32_t)(b * BN), da0 + off + 2 * ks, db0 + off + 2 * ks, idesc,
+                             kb > kb0 || ks > 0 ? 1u : 0u);
+            tc_commit_pair_mc(&bar->empty[s], pmask);
+            if (kb == kb1 - 1) tc_commit_pair_mc(&bar->acc_full[b], pmask);
+          }
+          if (++s == C::ST) s = 0;
         }
-        tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb, ++g) {
-          const int s = g % C::ST;
-          if (!mbar_wait_cluster(&bar->full[s], (uint32_t)(g / C::ST) & 1u)) {
-            set_device_error(err, kDevErrTimeoutFull);
-            ok = false;
-            break;
+        __syncwarp();
+      }
+      if (bad) break;
+    }
+  } else if (warp == 3 && half == 0) {
+    // ---------------------------------------------------------------- waits for the MMA warp
+    int s = 0, i = 0;
+    uint32_t ph = 0;
+    for (int64_t t = t0; t < tiles; t += tstep, ++i) {
+      bool bad = false;
+      for (int kb = kb0; kb < kb1;) {
+        if (kb == kb0 && i >= 2) {
+          if (!mbar_wait_cluster(&bar->acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1u)) {
+            if (lane == 0) set_device_error(err, kDevErrTimeoutAcc);
+            bad = true;
           }
           tc_fence_after();
-          const uint32_t st = base + (uint32_t)(s * C::kStage);
-#pragma unroll
-          for (int ks = 0; ks < BK / 32; ++ks)
-            mma_i8_ss_pair(tmem + (uint32_t)(b * BN), smem_desc_kmajor_sw128(st + (uint32_t)(ks * 32)),
-                           smem_desc_kmajor_sw128(st + C::kABytes + (uint32_t)(ks * 32)), idesc,
-                           kb > kb0 || ks > 0 ? 1u : 0u);
-          tc_commit_pair_mc(&bar->empty[s], pmask);
+          tc_fence_before();
         }
-        if (ok) tc_commit_pair_mc(&bar->acc_full[b], pmask);
+        const int end = min(kb + C::kBatch, kb1);
+        for (; kb < end; ++kb) {
+          if (!bad && !mbar_wait_cluster(&bar->full[s], ph)) {
+            if (lane == 0) set_device_error(err, kDevErrTimeoutFull);
+            bad = true;
+          }
+          if (++s == C::ST) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        // a lane may have run out of time where the others did not: all agree
+        if ((bad = named_barrier_or(kIssueBar, 64, bad))) break;
       }
+      if (bad) break;
     }
-    __syncwarp();
   } else if (warp >= kEpiWarp0) {
     // ---------------------------------------------------------------- epilogue
     const int ew = warp - kEpiWarp0;
@@ -517,8 +560,253 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
 }
 
+// Codes [rows, K] as boxes of 128 codes x `box` rows; what lies past K or the
+// rows reads as zero.
+bool codes_tmap(CUtensorMap* tm, const int8_t* x, int rows, int K, int64_t ld, int box) {
+  const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
+  const uint64_t strides[1] = {(uint64_t)(rows == 1 ? (K + 15) / 16 * 16 : ld)};
+  const uint32_t bx[2] = {BK, (uint32_t)box};
+  return make_tmap_nd(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, 2, dims, strides, bx, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// ------------------------------------------------------------------ streamed weights
+constexpr int kStreamThreads = 256;
+constexpr int kStreamRows = 128;          // output channels per tile: the MMA's M
+constexpr int kStreamRing = 108 * 1024;   // two CTAs per SM
+
+template <int NT>
+struct StreamCfg {
+  static constexpr int kW = kStreamRows * BK, kX = NT * BK;
+  static constexpr int kStage = kW + kX;
+  static constexpr int ST = kStreamRing / kStage;
+  static constexpr int kRing = ST * kStage;
+  static constexpr int kTmemCols = 2 * NT;
+  static constexpr int kSmem = 1024 + kRing + 1024 + NT * 4;   // alignment, ring, barriers, token scales
+  static_assert(kStreamRows * NT * 4 <= kRing, "partials fit where the ring was");
+};
+
+struct StreamBars {
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
+  uint32_t tmem_base;
+};
+
+template <int NT, class O>
+__global__ void __launch_bounds__(kStreamThreads, 2)
+    stream_kernel(const Matmul8Args p, int split, const __grid_constant__ CUtensorMap tmX,
+                  const __grid_constant__ CUtensorMap tmW, unsigned int* err) {
+  using C = StreamCfg<NT>;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* gbase = raw + (base - smem_u32(raw));
+  StreamBars* bar = reinterpret_cast<StreamBars*>(gbase + C::kRing);
+  float* sx = reinterpret_cast<float*>(gbase + C::kRing + 1024);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = split > 1 ? (int)cluster_ctarank() : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(&bar->full[s], 1);
+      mbar_init(&bar->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bar->acc_full[b], 1);
+      mbar_init(&bar->acc_empty[b], 4);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmW);
+  }
+  if (warp == 2) {
+    tmem_alloc(&bar->tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (threadIdx.x < NT) sx[threadIdx.x] = (int)threadIdx.x < p.M ? p.a_scale[threadIdx.x] : 0.0f;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+
+  const int tiles = (p.N + kStreamRows - 1) / kStreamRows;
+  const int nk = (p.K + BK - 1) / BK;
+  const int t0 = (int)blockIdx.x / split, tstep = split > 1 ? tiles : (int)gridDim.x;
+  const int kb0 = (int)((int64_t)q * nk / split), kb1 = (int)((int64_t)(q + 1) * nk / split);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int g = 0;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += tstep) {
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
+          const int s = g % C::ST;
+          if (g >= C::ST && !mbar_wait(&bar->empty[s], (uint32_t)(g / C::ST - 1) & 1u)) {
+            set_device_error(err, kDevErrTimeoutEmpty);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&bar->full[s], (uint32_t)C::kStage);
+          const uint32_t dst = base + (uint32_t)(s * C::kStage);
+          tma_load_2d(dst, &tmW, kb * BK, t * kStreamRows, &bar->full[s]);
+          tma_load_2d(dst + C::kW, &tmX, kb * BK, 0, &bar->full[s]);
+        }
+      }
+      for (int s = 0; s < C::ST && ok; ++s) {          // no copy or product is in flight any more
+        const int uses = (g - s + C::ST - 1) / C::ST;
+        if (uses > 0 && !mbar_wait(&bar->empty[s], (uint32_t)(uses - 1) & 1u)) {
+          set_device_error(err, kDevErrTimeoutDrain);
+          ok = false;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_i8(kStreamRows, NT);
+      const uint64_t da0 = smem_desc_kmajor_sw128(base), db0 = smem_desc_kmajor_sw128(base + C::kW);
+      int s = 0, i = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = t0; t < tiles && ok; t += tstep, ++i) {
+        const int b = i & 1;
+        if (i >= 2 && !mbar_wait(&bar->acc_empty[b], (uint32_t)(i / 2 - 1) & 1u)) {
+          set_device_error(err, kDevErrTimeoutAcc);
+          break;
+        }
+        tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&bar->full[s], ph)) {
+            set_device_error(err, kDevErrTimeoutFull);
+            ok = false;
+            break;
+          }
+          const uint64_t off = (uint64_t)(s * (C::kStage >> 4));   // descriptors count 16 bytes
+#pragma unroll
+          for (int ks = 0; ks < BK / 32; ++ks)
+            mma_i8_ss(tmem + (uint32_t)(b * NT), da0 + off + 2 * ks, db0 + off + 2 * ks, idesc,
+                      kb > kb0 || ks > 0 ? 1u : 0u);
+          tc_commit(&bar->empty[s]);
+          if (++s == C::ST) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok) tc_commit(&bar->acc_full[b]);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    constexpr int CH = NT < 32 ? NT : 32;
+    const int c = (warp - 4) * 32 + lane;              // this thread's channel of the tile
+    int i = 0;
+    for (int t = t0; t < tiles; t += tstep, ++i) {
+      const int b = i & 1;
+      const int64_t n = (int64_t)t * kStreamRows + c;
+      const auto* bias = static_cast<const typename O::elem*>(p.bias);
+      const float sw = n < p.N ? p.b_scale[n] : 0.0f;
+      const float bs = bias && n < p.N ? O::to(bias[n]) : 0.0f;
+      if (!mbar_wait(&bar->acc_full[b], (uint32_t)(i / 2) & 1u)) {
+        set_device_error(err, kDevErrTimeoutAcc);
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int ch = 0; ch < NT / CH; ++ch) {
+        uint32_t v[CH];
+        const uint32_t ta = tmem + ((uint32_t)((warp - 4) * 32) << 16) + (uint32_t)(b * NT + ch * CH);
+        if constexpr (CH == 16) tmem_ld_32x32b_x16(ta, v);
+        else tmem_ld_32x32b_x32(ta, v);
+        tmem_wait_ld();
+        if (split > 1) {
+#pragma unroll
+          for (int j = 0; j < CH; ++j)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + (uint32_t)(((ch * CH + j) * kStreamRows + c) * 4)), "r"(v[j])
+                         : "memory");
+        } else if (n < p.N) {
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            const int m = ch * CH + j;
+            if (m < p.M)
+              static_cast<typename O::elem*>(p.Y)[(int64_t)m * p.ldy + n] =
+                  O::from(dequant((int)v[j], sx[m], sw, p.inv_group, bs, bias != nullptr));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->acc_empty[b]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) {
+    cluster_sync();
+    // tokens m = q, q + S, ...: a thread per channel, two tokens at a time
+    const int c = threadIdx.x & (kStreamRows - 1), half = threadIdx.x / kStreamRows;
+    const int64_t n = (int64_t)t0 * kStreamRows + c;
+    const auto* bias = static_cast<const typename O::elem*>(p.bias);
+    const float sw = n < p.N ? p.b_scale[n] : 0.0f;
+    const float bs = bias && n < p.N ? O::to(bias[n]) : 0.0f;
+    for (int m = q + half * split; m < p.M; m += 2 * split) {
+      int v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        v[r] = 0;
+        if (r < split)
+          asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                       : "=r"(v[r])
+                       : "r"(map_to_rank(base, (uint32_t)r) + (uint32_t)((m * kStreamRows + c) * 4)));
+      }
+      const int acc = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+      if (n < p.N)
+        static_cast<typename O::elem*>(p.Y)[(int64_t)m * p.ldy + n] =
+            O::from(dequant(acc, sx[m], sw, p.inv_group, bs, bias != nullptr));
+    }
+    cluster_sync();                                    // the partials stay readable until every CTA has summed
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
 // ------------------------------------------------------------------ host side
-template <int NB, class O>
+template <int NT, class O>
+cudaError_t launch_stream(const Matmul8Args& a, int split, int sms, int dev, cudaStream_t st) {
+  using C = StreamCfg<NT>;
+  auto kern = stream_kernel<NT, O>;
+  static DeviceFlags configured;
+  cudaError_t e;
+  if (!configured.done(dev)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem)) != cudaSuccess)
+      return e;
+    configured.set(dev);
+  }
+  unsigned int* err = device_error_word();
+  if (!err) return cudaErrorInvalidDevicePointer;
+  CUtensorMap tX, tW;
+  if (!codes_tmap(&tX, a.A, a.M, a.K, a.lda, NT) || !codes_tmap(&tW, a.B, a.N, a.K, a.ldb, kStreamRows))
+    return cudaErrorInvalidValue;
+  const int tiles = (a.N + kStreamRows - 1) / kStreamRows;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min(tiles, 2 * sms)), 1, 1);
+  cfg.blockDim = dim3(kStreamThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a, split, tX, tW, err);
+}
+
+template <class O>
 cudaError_t launch_few(const Matmul8Args& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((a.N + kFewRows - 1) / kFewRows), 1, 1);
@@ -529,7 +817,34 @@ cudaError_t launch_few(const Matmul8Args& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<NB, O>, a);
+  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<O>, a);
+}
+
+// How many clusters of `size` CTAs of a kernel fit on the device at once (0
+// when the runtime cannot say), asked once per device and size.
+template <class Kernel>
+int resident_clusters(Kernel kern, int threads, int smem, int size, int dev, std::atomic<int> (&cache)[64][9]) {
+  std::atomic<int>* slot = dev >= 0 && dev < 64 ? &cache[dev][size] : nullptr;
+  if (slot) {
+    const int v = slot->load(std::memory_order_relaxed);
+    if (v > 0) return v - 1;
+  }
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)size, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  if (slot) slot->store(n + 1, std::memory_order_relaxed);
+  return n;
 }
 
 template <int BN, class O, bool SPLIT>
@@ -546,13 +861,8 @@ cudaError_t launch_tile(const Matmul8Args& a, const TilePlan& pl, int sms, int d
   unsigned int* err = device_error_word();
   if (!err) return cudaErrorInvalidDevicePointer;
   CUtensorMap tA, tB;
-  auto codes = [&](CUtensorMap* tm, const int8_t* x, int rows, int64_t ld, int box) {
-    const uint64_t dims[2] = {(uint64_t)a.K, (uint64_t)rows};
-    const uint64_t strides[1] = {(uint64_t)(rows == 1 ? (a.K + 15) / 16 * 16 : ld)};
-    const uint32_t bx[2] = {BK, (uint32_t)box};
-    return make_tmap_nd(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, 2, dims, strides, bx, CU_TENSOR_MAP_SWIZZLE_128B);
-  };
-  if (!codes(&tA, a.A, a.M, a.lda, BM) || !codes(&tB, a.B, a.N, a.ldb, C::kBRows)) return cudaErrorInvalidValue;
+  if (!codes_tmap(&tA, a.A, a.M, a.K, a.lda, BM) || !codes_tmap(&tB, a.B, a.N, a.K, a.ldb, C::kBRows))
+    return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)pl.tiles_m * pl.tiles_n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(SPLIT ? 2 * pl.split * tiles : 2 * std::min<int64_t>(tiles, sms / 2)), 1, 1);
@@ -571,27 +881,84 @@ cudaError_t launch_tile(const Matmul8Args& a, const TilePlan& pl, int sms, int d
   return cudaLaunchKernelEx(&cfg, kern, a, pl, tA, tB, err);
 }
 
+template <int BN, class O>
+int resident_tiles(int split, int dev) {
+  static std::atomic<int> cache[64][9];
+  return resident_clusters(tile_kernel<BN, O, true>, kTileThreads, TileCfg<BN>::kSmem, 2 * split, dev, cache);
+}
+template <int NT, class O>
+int resident_streams(int split, int dev) {
+  static std::atomic<int> cache[64][9];
+  return resident_clusters(stream_kernel<NT, O>, kStreamThreads, StreamCfg<NT>::kSmem, split, dev, cache);
+}
+
+// K slices of the streaming kernel: the fewest (1, 2, 4, 8) that give four
+// fifths of the SMs a CTA, as long as every cluster is resident at once and a
+// slice keeps two k-blocks.  16 tokens: 112 tiles (K = 4096) 13.6 us whole,
+// 15.4 in halves; 48 tiles (K = 4096) 10.0 in halves, 9.6 in quarters; 32 tiles
+// (K = 14336) 19.8 in halves, 14.3 in quarters, 14.8 in eighths.
+template <int NT, class O>
+cudaError_t launch_streamed(const Matmul8Args& a, int sms, int dev, cudaStream_t st) {
+  const int64_t tiles = ((int64_t)a.N + kStreamRows - 1) / kStreamRows;
+  const int nk = (a.K + BK - 1) / BK;
+  int split = 1;
+  while (split < 8 && tiles * split * 5 < (int64_t)sms * 4 && nk >= 4 * split &&
+         tiles <= resident_streams<NT, O>(2 * split, dev))
+    split *= 2;
+  return launch_stream<NT, O>(a, split, sms, dev, st);
+}
+
+// Tile width and K slices of the pair kernel by a model of its time in us: a
+// k-block costs 0.26 (256 x 128) or 0.30 (256 x 256) once its operands stream,
+// a launch 7 to 9 with its first loads and last epilogue, a split 1.5 for its
+// cluster barriers and sum; whole tiles walk in rounds of SMs / 2.  M = 256, K =
+// 12288, N = 4096: 37.7 whole at 256 wide, 24.0 in halves, 20.7 in thirds, 22.4 in
+// halves at 128 wide; clusters of 8 that are not all resident cost a second
+// round (34.4).
+template <class O>
+cudaError_t launch_tiled(const Matmul8Args& a, int sms, int dev, cudaStream_t st) {
+  const int tiles_m = (int)(((int64_t)a.M + 2 * BM - 1) / (2 * BM));
+  const int nk = (a.K + BK - 1) / BK;
+  const int pairs = sms / 2;
+  float best = 1e30f;
+  int bn = 256, split = 1;
+  for (int w : {256, 128}) {
+    const int64_t tiles = (int64_t)tiles_m * (((int64_t)a.N + w - 1) / w);
+    const float kb = w == 256 ? 0.30f : 0.26f, base = w == 256 ? 9.0f : 7.0f;
+    for (int s = 1; s <= 4; ++s) {
+      if (s > 1 && (tiles * s > pairs || nk < 2 * s)) break;
+      if (s > 1 && tiles > (w == 256 ? resident_tiles<256, O>(s, dev) : resident_tiles<128, O>(s, dev))) continue;
+      const float rounds = s > 1 ? 1.0f : (float)((tiles + pairs - 1) / pairs);
+      const float cost = rounds * (float)((nk + s - 1) / s) * kb + base + (s > 1 ? 1.5f : 0.0f);
+      if (cost < best) {
+        best = cost;
+        bn = w;
+        split = s;
+      }
+    }
+  }
+  const TilePlan pl{tiles_m, (int)(((int64_t)a.N + bn - 1) / bn), split};
+  if (bn == 128) return split > 1 ? launch_tile<128, O, true>(a, pl, sms, dev, st) : launch_tile<128, O, false>(a, pl, sms, dev, st);
+  return split > 1 ? launch_tile<256, O, true>(a, pl, sms, dev, st) : launch_tile<256, O, false>(a, pl, sms, dev, st);
+}
+
 template <class O>
 cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
-  if (a.M <= 8) return launch_few<1, O>(a, st);
-  if (a.M <= 16) return launch_few<2, O>(a, st);
-  if (a.M <= 32) return launch_few<4, O>(a, st);
+  // Up to 8 tokens and 24 MB of weights every load fits in flight at once (16.8
+  // MB: 5.1 us against 7.4 streamed); larger weights stream (58.7 MB: 18.5
+  // against 13.3).
+  if (a.M <= 8 && (int64_t)a.N * a.K <= (int64_t)24 << 20) return launch_few<O>(a, st);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
-  const int tiles_m = (a.M + 2 * BM - 1) / (2 * BM);
-  const int nk = (a.K + BK - 1) / BK;
-  const int n256 = (a.N + 255) / 256, n128 = (a.N + 127) / 128;
-  for (int s : {4, 2}) {
-    if (nk < 2 * s) continue;
-    if ((int64_t)tiles_m * n256 * s * 2 <= sms * 9 / 10 && (int64_t)tiles_m * n128 * s * 2 > sms * 9 / 10)
-      return launch_tile<256, O, true>(a, TilePlan{tiles_m, n256, s}, sms, dev, st);
-    if ((int64_t)tiles_m * n128 * s * 2 <= sms * 9 / 10)
-      return launch_tile<128, O, true>(a, TilePlan{tiles_m, n128, s}, sms, dev, st);
-  }
-  if ((int64_t)tiles_m * n128 * 2 <= sms) return launch_tile<128, O, false>(a, TilePlan{tiles_m, n128, 1}, sms, dev, st);
-  return launch_tile<256, O, false>(a, TilePlan{tiles_m, n256, 1}, sms, dev, st);
+  // Streamed weights up to 128 tokens: N = 28672, K = 4096, 128 tokens 28.9 us
+  // against 33.7 in pair tiles, N = K = 4096 11.7 against 13.9.
+  if (a.M <= 16) return launch_streamed<16, O>(a, sms, dev, st);
+  if (a.M <= 32) return launch_streamed<32, O>(a, sms, dev, st);
+  if (a.M <= 64) return launch_streamed<64, O>(a, sms, dev, st);
+  if (a.M <= 128) return launch_streamed<128, O>(a, sms, dev, st);
+  return launch_tiled<O>(a, sms, dev, st);
 }
 
 }  // namespace
