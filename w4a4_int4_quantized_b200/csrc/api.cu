@@ -374,7 +374,7 @@ w4a4_status w8a8_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* re
       !aligned16(Xq) || !aligned_to(x_scale, 4))
     return W4A4_ERR_MISALIGNED;
   if ((s = check_device()) != W4A4_OK) return s;
-  const RowQuantArgs a{X, residual, gamma, H, Xq, x_scale, ldx, ldr, ldh, ldq, M, K, group, eps};
+  const RowQuantArgs a{X, residual, gamma, H, Xq, x_scale, ldx, ldr, ldh, ldq, M, K, group, eps, 1.0f / (float)K};
   return cuda_status(launch_row_quantize(a, false, (int)dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -390,7 +390,7 @@ w4a4_status w8a8_silu_mul_quantize(const void* gate, int64_t ldg, const void* up
   if (!aligned_to(gate, es) || !aligned_to(up, es) || !aligned16(Xq) || !aligned_to(x_scale, 4))
     return W4A4_ERR_MISALIGNED;
   if ((s = check_device()) != W4A4_OK) return s;
-  const RowQuantArgs a{gate, up, nullptr, nullptr, Xq, x_scale, ldg, ldu, 0, ldq, M, K, group, 0.0f};
+  const RowQuantArgs a{gate, up, nullptr, nullptr, Xq, x_scale, ldg, ldu, 0, ldq, M, K, group, 0.0f, 0.0f};
   return cuda_status(launch_row_quantize(a, true, (int)dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 

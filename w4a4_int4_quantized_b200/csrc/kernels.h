@@ -77,7 +77,7 @@ struct RowQuantArgs {
   float* x_scale;          // [M]
   int64_t lda, ldb, ldh, ldq;
   int M, K, group;
-  float eps;
+  float eps, inv_k;        // inv_k = 1 / K
 };
 // dtype: 0 bf16, 1 fp16, 2 fp32
 cudaError_t launch_row_quantize(const RowQuantArgs& a, bool silu, int dtype, cudaStream_t st);

@@ -25,7 +25,11 @@
 #include "kernels.h"
 #include "plan_cache.h"
 
+#include <algorithm>
+
 namespace w4a4 {
+
+unsigned int* device_error_word();
 
 namespace {
 
@@ -120,10 +124,10 @@ __device__ __forceinline__ void store8(typename T::word* p, int n, const float2 
   }
 }
 
-// max that keeps a NaN of either side
-__device__ __forceinline__ float max_nan(float a, float b) {
+// max(m, |a|, |b|) that keeps a NaN of any of them
+__device__ __forceinline__ float max_abs(float m, float2 v) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(fabsf(v.x)), "f"(fabsf(v.y)));
   return d;
 }
 
@@ -199,13 +203,24 @@ __device__ __forceinline__ uint32_t pack_bytes4(uint32_t t0, uint32_t t1, uint32
   return __byte_perm(__byte_perm(t0, t1, 0x0040), __byte_perm(t2, t3, 0x0040), 0x5410);
 }
 
-// Codes of 8 elements.  Both ends of a bracket around 1 / s (2^-20 wide on
-// each side) rounding to one integer prove that the IEEE quotient rounds to it
-// too; otherwise, or where s is too small for its reciprocal, the quotient is
-// taken.
-__device__ __forceinline__ uint2 quantize8(const float2 (&f)[4], float s, float inv_lo, float inv_hi, bool exact) {
+// Codes of 8 elements by the quotient itself.
+__device__ __noinline__ uint2 quantize8_exact(float2 f0, float2 f1, float2 f2, float2 f3, float s) {
+  const float2 f[4] = {f0, f1, f2, f3};
+  uint32_t t[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    t[j] = (uint32_t)min(max(__float2int_rn(__fdiv_rn(j & 1 ? f[j >> 1].y : f[j >> 1].x, s)), -127), 127);
+  return make_uint2(pack_bytes4(t[0], t[1], t[2], t[3]), pack_bytes4(t[4], t[5], t[6], t[7]));
+}
+
+// Codes of 8 elements.  1 / s (one ulp off at most) moved by 2^-21 either way
+// brackets the IEEE quotient, whose rounding and the move's are 2^-24 each, and
+// adding 1.5 * 2^23 in one fused operation rounds to the integer: where both
+// ends agree the quotient rounds there too.  `bad` gathers disagreement (one
+// element in some 35,000), for which the quotient is taken.
+__device__ __forceinline__ uint2 quantize8(const float2 (&f)[4], float inv_lo, float inv_hi, uint32_t& bad) {
   const float2 mg = make_float2(kMagic, kMagic), ih = make_float2(inv_hi, inv_hi), il = make_float2(inv_lo, inv_lo);
-  uint32_t t[8], bad = exact ? 1u : 0u;
+  uint32_t t[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 a = __ffma2_rn(f[j], ih, mg), b = __ffma2_rn(f[j], il, mg);
@@ -213,33 +228,169 @@ __device__ __forceinline__ uint2 quantize8(const float2 (&f)[4], float s, float 
     t[2 * j + 1] = __float_as_uint(a.y);
     bad |= (t[2 * j] ^ __float_as_uint(b.x)) | (t[2 * j + 1] ^ __float_as_uint(b.y));
   }
-  if (bad) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      t[2 * j] = (uint32_t)min(max(__float2int_rn(__fdiv_rn(f[j].x, s)), -127), 127);
-      t[2 * j + 1] = (uint32_t)min(max(__float2int_rn(__fdiv_rn(f[j].y, s)), -127), 127);
-    }
-  }
   return make_uint2(pack_bytes4(t[0], t[1], t[2], t[3]), pack_bytes4(t[4], t[5], t[6], t[7]));
 }
 
-// silu(a) b with t = exp(-|a|) <= 1, so that neither side overflows before
-// the result does.
-__device__ __forceinline__ float silu_mul(float a, float b) {
-  const float t = expf(-fabsf(a));
-  return __fmul_rn(__fdividef(a >= 0.0f ? a : a * t, 1.0f + t), b);
+// silu(a) b = a b (a >= 0 ? 1 : t) / (1 + t) with t = exp(-|a|) <= 1, so that
+// nothing overflows before the result does.  t = 2^p (1 + e ln 2), where p is
+// -|a| log2(e) rounded and e what the rounding left out (an exact fused
+// residual, and log2(e)'s own low part): the argument's rounding would cost
+// |a| 2^-24 of t otherwise.  Errors of t: 2 ulp of ex2.approx and 2 roundings;
+// of the rest: 1 + t, 1 ulp of rcp.approx, 3 products.
+__device__ __forceinline__ float2 silu_mul2(float2 a, float2 b) {
+  constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
+  constexpr float kLn2 = 0.6931471805599453f;
+  const float2 x = make_float2(-fabsf(a.x), -fabsf(a.y));
+  const float2 l = make_float2(kLog2e, kLog2e), ll = make_float2(kLog2eLow, kLog2eLow), ln2 = make_float2(kLn2, kLn2);
+  const float2 p = __fmul2_rn(x, l);
+  const float2 np = make_float2(-p.x, -p.y);
+  const float2 e = __ffma2_rn(x, ll, __ffma2_rn(x, l, np));
+  float2 t0;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(t0.x) : "f"(p.x));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(t0.y) : "f"(p.y));
+  const float2 t = __ffma2_rn(__fmul2_rn(t0, e), ln2, t0);
+  const float2 d = __fadd2_rn(t, make_float2(1.0f, 1.0f));
+  float2 r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  const float2 g = make_float2(a.x >= 0.0f ? 1.0f : t.x, a.y >= 0.0f ? 1.0f : t.y);
+  return __fmul2_rn(__fmul2_rn(__fmul2_rn(a, r), g), b);
+}
+
+// How far into a row an element at e is: 8 or more where every chunk is whole.
+template <bool FULL>
+__device__ __forceinline__ int left(int K, int e) {
+  return FULL ? 8 : K - e;
+}
+
+// A row whose 8 VPT elements per thread are in f: for OP 0 the sum before the
+// norm, for OP 1 the gated product.  FULL: every thread has all of its chunks
+// inside the row.  gamma(v, g) gives the weights of chunk v; taken() runs in
+// every thread once all of the row's threads have their inputs in registers.
+template <class T, int OP, int VPT, bool VEC, bool FULL, class Gamma, class Taken>
+__device__ __forceinline__ void finish_row(float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t, int tpr,
+                                           int nwarps, float (*red)[32], Gamma&& gamma, Taken&& taken) {
+  using W = typename T::word;
+  const int lane = threadIdx.x & 31;
+  if constexpr (OP == 0) {
+    if (p.H) {
+      W* h = static_cast<W*>(p.H) + row * p.ldh;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int e = (v * tpr + t) * 8;
+        store8<T, VEC>(h + e, left<FULL>(p.K, e), f[v]);
+      }
+    }
+    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(f[v][j], f[v][j], s2);
+    float ss = row_sum(__fadd_rn(s2.x, s2.y), red[0], nwarps);
+    taken();
+    float eps = p.eps;
+    if (!(ss <= 3.4e38f)) {   // the same value in every thread of the row
+      float m = 0.0f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max_abs(m, f[v][j]);
+      m = row_max(m, red[2], nwarps);
+      // an infinity or a NaN stays one through all that follows
+      const float k = m < __int_as_float(0x7F800000) ? exp2f(1.0f - (float)ilogbf(m)) : 1.0f;
+      s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[v][j].x *= k;
+          f[v][j].y *= k;
+          s2 = __ffma2_rn(f[v][j], f[v][j], s2);
+        }
+      ss = row_sum(__fadd_rn(s2.x, s2.y), red[0], nwarps);
+      eps = eps * k * k;
+    }
+    // 1 / sqrt(x): the hardware's estimate (2 ulp) and one Newton step
+    const float x = fmaf(ss, p.inv_k, eps);
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    r = fmaf(0.5f * r, fmaf(-x * r, r, 1.0f), r);
+    const float2 r2 = make_float2(r, r);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], r2);
+      if (p.gamma) {
+        float2 g[4];
+        gamma(v, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], g[j]);
+      }
+    }
+  }
+  if (p.group) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) rotate8(f[v], p.group, lane);
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max_abs(m, f[v][j]);
+  m = row_max(m, red[1], nwarps);
+  if constexpr (OP == 1) taken();
+  const bool finite = m < __int_as_float(0x7F800000);
+  const float s = finite ? __fdiv_rn(m, 127.0f) : __int_as_float(0x7FC00000);
+  if (t == 0) p.x_scale[row] = s;
+  // Codes are 0 in a row of zeros and in one whose scale is NaN; a scale too
+  // small for its reciprocal takes the quotients.
+  const bool some = s > 0.0f, tiny = s < 0x1p-100f;
+  const uint32_t keep = some ? 0xFFFFFFFFu : 0u;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(tiny || !some ? 1.0f : s));
+  const float inv_hi = __fmul_rn(inv, 1.0f + 0x1p-21f), inv_lo = __fmul_rn(inv, 1.0f - 0x1p-21f);
+  uint32_t bad = tiny ? 1u : 0u;
+  uint2 w[VPT];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) w[v] = quantize8(f[v], inv_lo, inv_hi, bad);
+  if (bad & keep) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) w[v] = quantize8_exact(f[v][0], f[v][1], f[v][2], f[v][3], s);
+  }
+  int8_t* q = p.Xq + row * p.ldq;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = (v * tpr + t) * 8;
+    const int n = left<FULL>(p.K, e);
+    w[v].x &= keep;
+    w[v].y &= keep;
+    if (FULL || n >= 8) {
+      *reinterpret_cast<uint2*>(q + e) = w[v];
+    } else if (!VEC) {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (j < n) q[e + j] = (int8_t)((j < 4 ? w[v].x >> (8 * j) : w[v].y >> (8 * j - 32)) & 0xFFu);
+    }
+  }
+}
+
+// The second operand into f: added (OP 0) or gated by it (OP 1).
+template <int OP>
+__device__ __forceinline__ void combine8(float2 (&f)[4], const float2 (&g)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = OP == 0 ? __fadd2_rn(f[j], g[j]) : silu_mul2(f[j], g[j]);
 }
 
 // OP 0: norm (A = x, B = residual or null, gamma, H or null); OP 1: silu (A =
-// gate, B = up).  VPT: chunks of 8 per thread; MAXT: most threads of a block.
+// gate, B = up).  VPT: chunks of 8 per thread.  Rows straight from global
+// memory: few rows, rows off the 16-byte alignment (VEC false), rows whose
+// inputs do not fit in shared memory.
 template <class T, int OP, int VPT, int MAXT, bool VEC>
 __global__ void __launch_bounds__(MAXT) row_quantize_kernel(RowQuantArgs p, int tpr) {
   using W = typename T::word;
   __shared__ float red[3][32];
   const int rpb = blockDim.x / tpr;            // > 1 only where a row is one warp
-  const int nwarps = tpr >> 5;
   const int t = threadIdx.x % tpr;
-  const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
   for (int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr; row < p.M; row += (int64_t)gridDim.x * rpb) {
@@ -257,145 +408,239 @@ __global__ void __launch_bounds__(MAXT) row_quantize_kernel(RowQuantArgs p, int 
         const int e = (v * tpr + t) * 8;
         float2 g[4];
         load8<T, VEC>(b + e, p.K - e, g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (OP == 0) f[v][j] = __fadd2_rn(f[v][j], g[j]);
-          else f[v][j] = make_float2(silu_mul(f[v][j].x, g[j].x), silu_mul(f[v][j].y, g[j].y));
-        }
+        combine8<OP>(f[v], g);
       }
     }
-    if (OP == 0) {
-      if (p.H) {
-        W* h = static_cast<W*>(p.H) + row * p.ldh;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
+    finish_row<T, OP, VPT, VEC, false>(
+        f, p, row, t, tpr, tpr >> 5, red,
+        [&](int v, float2 (&g)[4]) {
           const int e = (v * tpr + t) * 8;
-          store8<T, VEC>(h + e, p.K - e, f[v]);
-        }
-      }
-      float2 s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(f[v][j], f[v][j], s2);
-      float ss = row_sum(__fadd_rn(s2.x, s2.y), red[0], nwarps);
-      float eps = p.eps;
-      if (!(ss <= 3.4e38f)) {   // the same value in every thread of the row
-        float m = 0.0f;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) m = max_nan(m, max_nan(fabsf(f[v][j].x), fabsf(f[v][j].y)));
-        m = row_max(m, red[2], nwarps);
-        // an infinity or a NaN stays one through all that follows
-        const float k = m < __int_as_float(0x7F800000) ? exp2f(1.0f - (float)ilogbf(m)) : 1.0f;
-        s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[v][j].x *= k;
-            f[v][j].y *= k;
-            s2 = __ffma2_rn(f[v][j], f[v][j], s2);
-          }
-        ss = row_sum(__fadd_rn(s2.x, s2.y), red[0], nwarps);
-        eps = eps * k * k;
-      }
-      const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)p.K), eps)));
-      const float2 r2 = make_float2(r, r);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int e = (v * tpr + t) * 8;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], r2);
-        if (p.gamma) {
-          float2 g[4];
           load8<T, VEC>(static_cast<const W*>(p.gamma) + e, p.K - e, g);
+        },
+        [] {});
+  }
+}
+
+// Bytes of a contiguous row into shared memory, completing on a barrier (16-byte
+// aligned addresses and sizes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// 8 elements from shared memory (16-byte aligned), zeros where n <= 0.
+template <class T>
+__device__ __forceinline__ void smem8(uint32_t addr, int n, float2 (&f)[4]) {
+  uint32_t u[T::kWords];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], g[j]);
-        }
-      }
-    }
-    if (p.group) {
+  for (int i = 0; i < T::kWords / 4; ++i) {
+    u[4 * i] = u[4 * i + 1] = u[4 * i + 2] = u[4 * i + 3] = 0u;
+    if (n > 0)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u[4 * i]), "=r"(u[4 * i + 1]), "=r"(u[4 * i + 2]), "=r"(u[4 * i + 3])
+                   : "r"(addr + 16 * i));
+  }
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) rotate8(f[v], p.group, lane);
-    }
-    float m = 0.0f;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m = max_nan(m, max_nan(fabsf(f[v][j].x), fabsf(f[v][j].y)));
-    m = row_max(m, red[1], nwarps);
-    const bool finite = m < __int_as_float(0x7F800000);
-    const float s = finite ? __fdiv_rn(m, 127.0f) : __int_as_float(0x7FC00000);
-    if (t == 0) p.x_scale[row] = s;
-    const bool some = s > 0.0f;               // false for a row of zeros and for a NaN
-    const bool exact = s < 0x1p-100f;
-    const float inv = __frcp_rn(exact || !some ? 1.0f : s);
-    const float inv_hi = __fmul_rn(inv, 1.0f + 0x1p-20f), inv_lo = __fmul_rn(inv, 1.0f - 0x1p-20f);
-    int8_t* q = p.Xq + row * p.ldq;
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (T::kWords == 4) f[j] = T::two(u[j]);
+    else f[j] = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+  }
+}
+
+// Many aligned rows: persistent blocks, each row's inputs brought into a ring
+// of `stages` rows in shared memory by bulk copies, so that the next rows
+// arrive while one is worked on and no register holds a load in flight.  A
+// team of tpr threads owns a ring; with rows of one warp a block has several.
+constexpr int kRingStages = 4, kRingTeams = 4;
+constexpr int kRingThreads = 768;          // threads of an SM (1024 where rows are too wide for fewer)
+
+template <class T, int OP, int VPT, int MAXT, bool FULL>
+__global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAXT : 1)
+    row_ring_kernel(RowQuantArgs p, int tpr, int stages, unsigned int* err) {
+  using W = typename T::word;
+  // the weights of a thread's elements stay in registers, packed, where they fit
+  constexpr bool kHoldGamma = OP == 0 && T::kWords == 4 && MAXT < 1024;
+  extern __shared__ __align__(128) uint8_t ring_raw[];
+  __shared__ float red[3][32];
+  __shared__ __align__(8) uint64_t full[kRingTeams][kRingStages];
+  const int rpb = blockDim.x / tpr;
+  const int team = threadIdx.x / tpr, t = threadIdx.x % tpr;
+  const uint32_t row_bytes = (uint32_t)p.K * sizeof(W);
+  const uint32_t stage_bytes = p.B ? 2 * row_bytes : row_bytes;
+  const uint32_t ring = smem_u32(ring_raw) + (uint32_t)(team * stages) * stage_bytes;
+  const int64_t row0 = (int64_t)blockIdx.x * rpb + team, step = (int64_t)gridDim.x * rpb;
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[team][s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  auto issue = [&](int64_t row, int s) {
+    mbar_arrive_expect_tx(&full[team][s], stage_bytes);
+    const uint32_t dst = ring + (uint32_t)s * stage_bytes;
+    bulk_load(dst, static_cast<const W*>(p.A) + row * p.lda, row_bytes, &full[team][s]);
+    if (p.B) bulk_load(dst + row_bytes, static_cast<const W*>(p.B) + row * p.ldb, row_bytes, &full[team][s]);
+  };
+  if (t == 0)
+    for (int s = 0; s < stages; ++s)
+      if (row0 + s * step < p.M) issue(row0 + s * step, s);
+  uint4 gw[kHoldGamma ? VPT : 1];
+  if (kHoldGamma && p.gamma) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int e = (v * tpr + t) * 8;
-      const int n = p.K - e;
-      if (n <= 0) continue;
-      uint2 w = some ? quantize8(f[v], s, inv_lo, inv_hi, exact) : make_uint2(0u, 0u);
-      if (n >= 8) {
-        *reinterpret_cast<uint2*>(q + e) = w;
-      } else {
+      gw[v] = left<FULL>(p.K, e) > 0 ? *reinterpret_cast<const uint4*>(static_cast<const W*>(p.gamma) + e)
+                                     : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  int s = 0;
+  uint32_t ph = 0;
+  for (int64_t row = row0; row < p.M; row += step) {
+    if (!mbar_wait(&full[team][s], ph)) set_device_error(err, kDevErrTimeoutFull);
+    const uint32_t src = ring + (uint32_t)s * stage_bytes;
+    float2 f[VPT][4];
 #pragma unroll
-        for (int j = 0; j < 7; ++j)
-          if (j < n) q[e + j] = (int8_t)((j < 4 ? w.x >> (8 * j) : w.y >> (8 * j - 32)) & 0xFFu);
+    for (int v = 0; v < VPT; ++v) {
+      const int e = (v * tpr + t) * 8;
+      smem8<T>(src + (uint32_t)e * sizeof(W), left<FULL>(p.K, e), f[v]);
+      if (p.B) {
+        float2 g[4];
+        smem8<T>(src + row_bytes + (uint32_t)e * sizeof(W), left<FULL>(p.K, e), g);
+        combine8<OP>(f[v], g);
       }
+    }
+    // the row's sum or maximum depends on everything that its threads read
+    // here, so once it is known the stage takes the row after next
+    finish_row<T, OP, VPT, true, FULL>(
+        f, p, row, t, tpr, tpr >> 5, red,
+        [&](int v, float2 (&g)[4]) {
+          if constexpr (kHoldGamma) {
+            g[0] = T::two(gw[v].x);
+            g[1] = T::two(gw[v].y);
+            g[2] = T::two(gw[v].z);
+            g[3] = T::two(gw[v].w);
+          } else {
+            const int e = (v * tpr + t) * 8;
+            load8<T, true>(static_cast<const W*>(p.gamma) + e, left<FULL>(p.K, e), g);
+          }
+        },
+        [&] {
+          if (t == 0 && row + stages * step < p.M) {
+            fence_proxy_async_smem();
+            issue(row + stages * step, s);
+          }
+        });
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
     }
   }
 }
 
-template <class T, int OP, int VPT, int MAXT, bool VEC>
-cudaError_t launch_t(const RowQuantArgs& a, int tpr, int rpb, int grid, cudaStream_t st) {
+// ------------------------------------------------------------------ host side
+template <class Kernel, class... Args>
+cudaError_t launch_rows(Kernel kern, int64_t grid, int threads, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(tpr * rpb, 1, 1);
+  cfg.gridDim = dim3((unsigned)(grid < 0x7FFFFFFF ? grid : 0x7FFFFFFF), 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, row_quantize_kernel<T, OP, VPT, MAXT, VEC>, a, tpr);
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
+
+int threads_per_row(int chunks, int vpt) { return ((chunks + vpt - 1) / vpt + 31) / 32 * 32; }
 
 template <class T, int OP, bool VEC>
-cudaError_t launch_v(const RowQuantArgs& a, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
+cudaError_t launch_direct(const RowQuantArgs& a, int vpt, cudaStream_t st) {
   const int chunks = (a.K + 7) / 8;
-  // Few rows (at most two per SM): a chunk per thread, the shortest chain.
-  // Otherwise up to four per thread.
-  int vpt = a.M <= 2 * sms ? 1 : 4;
   while (vpt < 4 && (chunks + vpt - 1) / vpt > 1024) vpt *= 2;
   while (vpt > 1 && chunks <= 32 * (vpt / 2)) vpt /= 2;
-  const int tpr = ((chunks + vpt - 1) / vpt + 31) / 32 * 32;
+  const int tpr = threads_per_row(chunks, vpt);
   const int rpb = tpr == 32 ? 4 : 1;
-  const int64_t blocks = (a.M + rpb - 1) / rpb;
-  const int grid = (int)(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF);
-  if (vpt == 1) return launch_t<T, OP, 1, 1024, VEC>(a, tpr, rpb, grid, st);
-  if (vpt == 2) return launch_t<T, OP, 2, 1024, VEC>(a, tpr, rpb, grid, st);
-  if (tpr <= 512) return launch_t<T, OP, 4, 512, VEC>(a, tpr, rpb, grid, st);
-  return launch_t<T, OP, 4, 1024, VEC>(a, tpr, rpb, grid, st);
+  const int64_t blocks = ((int64_t)a.M + rpb - 1) / rpb;
+  if (vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 1024, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
+  if (vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 1024, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
+  if (tpr <= 512) return launch_rows(row_quantize_kernel<T, OP, 4, 512, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
+  return launch_rows(row_quantize_kernel<T, OP, 4, 1024, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
 }
 
-template <class T>
-cudaError_t launch_type(const RowQuantArgs& a, bool silu, cudaStream_t st) {
+constexpr int kRingBytes = 200 * 1024;     // of an SM's shared memory
+
+struct RingPlan {
+  int vpt, tpr, rpb, stages, per_sm;
+};
+
+// Threads per row, rings and their depth for rows of `stage` bytes.  Four chunks
+// per thread where 384 threads then cover the row (a thread's share of the two
+// reductions is some 120 instructions), else the fewest that 1024 threads allow.
+bool plan_ring(int K, size_t stage, RingPlan& pl) {
+  const int chunks = K / 8;
+  int vpt = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
+  if (chunks > 4 * 384) vpt = chunks <= 1024 * 2 ? 2 : 4;
+  const int tpr = threads_per_row(chunks, vpt);
+  const int rpb = tpr == 32 ? kRingTeams : 1;
+  const int per_sm = (int)std::min<size_t>(kRingBytes / (2 * stage * rpb), std::max(1, kRingThreads / (tpr * rpb)));
+  if (per_sm < 1) return false;
+  pl = RingPlan{vpt, tpr, rpb, (int)std::min<size_t>(kRingStages, kRingBytes / (stage * rpb * per_sm)), per_sm};
+  return true;
+}
+
+template <class T, int OP, int VPT, int MAXT, bool FULL>
+cudaError_t launch_ring_t(const RowQuantArgs& a, const RingPlan& pl, size_t stage, int sms, int dev, cudaStream_t st) {
+  auto kern = row_ring_kernel<T, OP, VPT, MAXT, FULL>;
+  static DeviceFlags configured;
+  cudaError_t e;
+  if (!configured.done(dev)) {
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)) != cudaSuccess) return e;
+    configured.set(dev);
+  }
+  unsigned int* err = device_error_word();
+  if (!err) return cudaErrorInvalidDevicePointer;
+  const int64_t teams = ((int64_t)a.M + pl.rpb - 1) / pl.rpb;
+  return launch_rows(kern, std::min<int64_t>(teams, (int64_t)sms * pl.per_sm), pl.tpr * pl.rpb,
+                     stage * pl.rpb * pl.stages, st, a, pl.tpr, pl.stages, err);
+}
+
+template <class T, int OP, int VPT, int MAXT>
+cudaError_t launch_ring(const RowQuantArgs& a, const RingPlan& pl, size_t stage, int sms, int dev, cudaStream_t st) {
+  return a.K == 8 * VPT * pl.tpr ? launch_ring_t<T, OP, VPT, MAXT, true>(a, pl, stage, sms, dev, st)
+                                 : launch_ring_t<T, OP, VPT, MAXT, false>(a, pl, stage, sms, dev, st);
+}
+
+template <class T, int OP>
+cudaError_t launch_op(const RowQuantArgs& a, cudaStream_t st) {
   const size_t es = sizeof(typename T::word);
   auto rows16 = [&](const void* p, int64_t ld) {
     return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (a.M == 1 || (uint64_t)ld * es % 16 == 0));
   };
   const bool vec = a.K % 8 == 0 && rows16(a.A, a.lda) && rows16(a.B, a.ldb) && rows16(a.H, a.ldh) && rows16(a.gamma, 0);
-  if (silu) return vec ? launch_v<T, 1, true>(a, st) : launch_v<T, 1, false>(a, st);
-  return vec ? launch_v<T, 0, true>(a, st) : launch_v<T, 0, false>(a, st);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
+  // Few rows (at most two per SM): a chunk per thread, the shortest chain.
+  const int vpt = a.M <= 2 * sms ? 1 : 4;
+  if (!vec) return launch_direct<T, OP, false>(a, vpt, st);
+  RingPlan pl;
+  const size_t stage = (size_t)a.K * es * (a.B ? 2 : 1);
+  if (a.M <= 2 * sms || !plan_ring(a.K, stage, pl)) return launch_direct<T, OP, true>(a, vpt, st);
+  if (pl.vpt == 1) return launch_ring<T, OP, 1, 384>(a, pl, stage, sms, dev, st);
+  if (pl.vpt == 2 && pl.tpr <= 384) return launch_ring<T, OP, 2, 384>(a, pl, stage, sms, dev, st);
+  if (pl.vpt == 2) return launch_ring<T, OP, 2, 1024>(a, pl, stage, sms, dev, st);
+  if (pl.tpr <= 384) return launch_ring<T, OP, 4, 384>(a, pl, stage, sms, dev, st);
+  return launch_ring<T, OP, 4, 1024>(a, pl, stage, sms, dev, st);
+}
+
+template <class T>
+cudaError_t launch_type(const RowQuantArgs& a, bool silu, cudaStream_t st) {
+  return silu ? launch_op<T, 1>(a, st) : launch_op<T, 0>(a, st);
 }
 
 }  // namespace
