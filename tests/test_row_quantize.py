@@ -4,16 +4,20 @@
 Tolerances, with u = 2^-24 (half a step of fp32, relative):
   norm  y carries h's own rounding (1 u), the sum of squares (a chain of at
         most 16 fused adds in a thread, 1 add, 10 adds across the row, 2 u
-        from h: 29 u), the division and eps (2 u), halved by the square root
-        (1 u more), reciprocal, product with h and with gamma (1 u each):
-        at most 21 u of |y|.
-  silu  expf 2 ulp (4 u) in numerator and denominator, 1 + t, a t and the
-        product (1 u each), the division 2 ulp (4 u): at most 15 u of |y|.
+        from h: 29 u), its product with 1 / K and eps (3 u), halved by the
+        square root, whose Newton step leaves 1.5 u, the products with gamma
+        and with the factor (1 u each): at most 21 u of |y|.
+  silu  t = 2^(-a log2 e): the exponent's two roundings put 1.5 |a| u into t and
+        ex2.approx 4 u, of which t / (1 + t) reaches y: for a >= 0 at most 2 u +
+        0.5 u, for a < 0 all of it; 1 + t (1 u), rcp.approx 1 ulp (2 u), two
+        products (2 u): at most 9 u + 1.5 max(0, -a) u of |y|.  Gates below -87
+        count as 0.
   rotation  a sum of g values in log2 g roundings: at most (c + log2 g) u of
         the group's sum of |y|.
 With D the largest such error of a row, the scale is off by at most
-D / 127 + u s, and y / s by at most 2 * 127 D / max|y| + 4 * 127 u, so a code is
-within half a step plus that of the 64-bit quotient."""
+D / 127 + u s, and y / s by at most 2 * 127 D / max|y| + 4 * 127 u (1 / s by
+rcp.approx 2 u, s and the factor 1 u each), so a code is within half a step plus
+that of the 64-bit quotient."""
 from __future__ import annotations
 
 import numpy as np
@@ -43,16 +47,20 @@ def silu64(a, b):
     return a / (1.0 + np.exp(-a)) * b
 
 
+def silu_c(a):
+    return 9 + 1.5 * np.maximum(0.0, -a)
+
+
 def check_codes(y, g, c, q, s):
-    """Codes q and scales s of the 64-bit rows y, c u of relative error in y."""
+    """Codes q and scales s of the 64-bit rows y, c u of relative error in y (a
+    number, or one for each element)."""
     M, K = y.shape
     mag = np.abs(y)
     if g:
-        l1 = mag.reshape(M, K // g, g).sum(axis=2).max(axis=1)
+        D = U * ((c + np.log2(g)) * mag).reshape(M, K // g, g).sum(axis=2).max(axis=1)
         y = hadamard(y, g)
-        D = (c + np.log2(g)) * U * l1
     else:
-        D = c * U * mag.max(axis=1)
+        D = U * (c * mag).max(axis=1)
     amax = np.abs(y).max(axis=1)
     s64 = amax / 127.0
     assert np.all(np.abs(s - s64) <= D / 127.0 + U * s64 + 2.0 ** -149)
@@ -231,7 +239,7 @@ def test_silu(M, K, group, pad, offset, dtype):
         up[3] = 0
     q, s = w4.w8a8_silu_mul_quantize(gate, up, group)
     torch.cuda.synchronize()
-    check_codes(silu64(_f64(gate), _f64(up)), group, 15, _f64(q), _f64(s))
+    check_codes(silu64(_f64(gate), _f64(up)), group, silu_c(_f64(gate)), _f64(q), _f64(s))
 
 
 @gpu
@@ -285,9 +293,67 @@ def test_small_values(small):
     q, s, _ = w4.w8a8_add_rmsnorm_quantize(X, None, 1e-30)
     check_codes(norm64(_f64(X), None, None, float(np.float32(1e-30)))[1], 0, 21, _f64(q), _f64(s))
     q, s = w4.w8a8_silu_mul_quantize(X, one)
-    check_codes(silu64(_f64(X), _f64(one)), 0, 15, _f64(q), _f64(s))
+    check_codes(silu64(_f64(X), _f64(one)), 0, silu_c(_f64(X)), _f64(q), _f64(s))
     q, s = w4.w8a8_silu_mul_quantize(one, X)
-    check_codes(silu64(_f64(one), _f64(X)), 0, 15, _f64(q), _f64(s))
+    check_codes(silu64(_f64(one), _f64(X)), 0, silu_c(_f64(one)), _f64(q), _f64(s))
+
+
+@gpu
+@pytest.mark.parametrize("M", [3, 400])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_extreme_gates(M, dtype):
+    """Finite gates to either end of the type: no row turns into NaN, strongly
+    negative ones count as 0 and the rest keeps its values."""
+    import torch
+    dt = _dt(dtype)
+    K = 512
+    gate, up = _rows(_data(M, K, 50), dt), _rows(_data(M, K, 51), dt)
+    gate[:, 3] = torch.finfo(dt).min
+    gate[:, 5], gate[:, 6], gate[:, 7] = -90.0, -1000.0, -85.0
+    gate[1], up[1] = torch.finfo(dt).min, 1.0
+    gate[2], up[2] = torch.finfo(dt).max, 1.0
+    q, s = w4.w8a8_silu_mul_quantize(gate, up)
+    assert s[1] == 0 and not q[1].any()
+    assert (q[2] == 127).all() and abs(float(s[2]) * 127 / torch.finfo(dt).max - 1) < 20 * U
+    a = _f64(gate)
+    with np.errstate(over="ignore"):
+        y = np.where(a < -87.0, 0.0, silu64(np.maximum(a, -87.0), _f64(up)))
+    keep = [m for m in range(M) if m not in (1, 2)]
+    check_codes(y[keep], 0, silu_c(np.maximum(a, -87.0))[keep], _f64(q)[keep], _f64(s)[keep])
+
+
+@gpu
+@pytest.mark.parametrize("K", [512, 4096, 5120, 12288])
+def test_many_rows_of_unlike_size(K):
+    """Neighbouring rows a million apart in size: a maximum taken from another
+    row would show."""
+    import torch
+    M = 3000
+    x = _data(M, K, 60)
+    x *= 10.0 ** np.random.default_rng(61).integers(-3, 4, M)[:, None]
+    X = _rows(x, torch.bfloat16)
+    one = torch.ones_like(X)
+    for _ in range(3):
+        q, s = w4.w8a8_silu_mul_quantize(one, X)
+        q2, s2, _ = w4.w8a8_add_rmsnorm_quantize(X, None, EPS)
+        check_codes(silu64(_f64(one), _f64(X)), 0, silu_c(_f64(one)), _f64(q), _f64(s))
+        check_codes(norm64(_f64(X), None, None, EPS)[1], 0, 21, _f64(q2), _f64(s2))
+
+
+@gpu
+@pytest.mark.parametrize("M", [4, 400])
+@pytest.mark.parametrize("group", [0, 128])
+def test_weights_of_extreme_size(M, group):
+    """Weights whose product with h leaves fp32's range although y does not, and
+    ones that make every y tiny."""
+    import torch
+    K = 1024
+    X = _rows(_data(M, K, 70, 1e6), torch.float32)
+    for size in (1e33, 1e-33, 1e-36):
+        gamma = torch.full((K,), size, device="cuda")
+        q, s, _ = w4.w8a8_add_rmsnorm_quantize(X, gamma, EPS, group)
+        torch.cuda.synchronize()
+        check_codes(norm64(_f64(X), None, _f64(gamma), EPS)[1], group, 21, _f64(q), _f64(s))
 
 
 @gpu

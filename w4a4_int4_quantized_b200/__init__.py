@@ -301,14 +301,13 @@ def _codes_out(M, K, like):
     return _torch.empty((M, (K + 15) // 16 * 16), dtype=_torch.int8, device=like.device)[:, :K]
 
 
-def _run(fn, core, dev, stream, *args):
-    """core(*args, dev, raw stream) with the tensors' device current; outputs
-    that core allocates belong to the stream that it launches on."""
+def _elsewhere(fn, core, dev, stream, args):
+    """core(*args) off the common path: tensors of another device than the
+    current one, or a stream that was given; outputs that core allocates belong
+    to the stream that it launches on."""
     if dev < 0:
         raise W4A4Error(fn, 6)
     if stream is None:
-        if dev == _cur_device():
-            return core(*args, dev, _raw_stream(dev))
         with _torch.cuda.device(dev):
             return core(*args, dev, _raw_stream(dev))
     if stream.device.index != dev:
@@ -354,8 +353,11 @@ def w8a8_add_rmsnorm_quantize(X, gamma, eps, group=0, residual=None, H=None, Xq=
     have their rows 16-byte aligned (a stride of K rounded up)."""
     if _torch is None:
         _bind_torch()
-    return _run("w8a8_add_rmsnorm_quantize", _add_rmsnorm_quantize, X.get_device(), stream, X, gamma, eps, group,
-                residual, H, Xq, x_scale)
+    dev = X.get_device()
+    if stream is None and dev >= 0 and dev == _cur_device():
+        return _add_rmsnorm_quantize(X, gamma, eps, group, residual, H, Xq, x_scale, dev, _raw_stream(dev))
+    return _elsewhere("w8a8_add_rmsnorm_quantize", _add_rmsnorm_quantize, dev, stream,
+                      (X, gamma, eps, group, residual, H, Xq, x_scale))
 
 
 def _silu_mul_quantize(gate, up, group, Xq, x_scale, dev, st):
@@ -382,7 +384,10 @@ def w8a8_silu_mul_quantize(gate, up, group=0, Xq=None, x_scale=None, stream=None
     rows of any stride: the halves of one [M, 2 K] product need no copy."""
     if _torch is None:
         _bind_torch()
-    return _run("w8a8_silu_mul_quantize", _silu_mul_quantize, gate.get_device(), stream, gate, up, group, Xq, x_scale)
+    dev = gate.get_device()
+    if stream is None and dev >= 0 and dev == _cur_device():
+        return _silu_mul_quantize(gate, up, group, Xq, x_scale, dev, _raw_stream(dev))
+    return _elsewhere("w8a8_silu_mul_quantize", _silu_mul_quantize, dev, stream, (gate, up, group, Xq, x_scale))
 
 
 def _matmul8(Xq, x_scale, Wq, w_scale, group, bias, Y, dtype, dev, st):
@@ -413,7 +418,10 @@ def w8a8_matmul(Xq, x_scale, Wq, w_scale, group=0, bias=None, Y=None, dtype=None
     matrices have rows a multiple of 16 bytes apart, Y rows of any stride."""
     if _torch is None:
         _bind_torch()
-    return _run("w8a8_matmul", _matmul8, Xq.get_device(), stream, Xq, x_scale, Wq, w_scale, group, bias, Y, dtype)
+    dev = Xq.get_device()
+    if stream is None and dev >= 0 and dev == _cur_device():
+        return _matmul8(Xq, x_scale, Wq, w_scale, group, bias, Y, dtype, dev, _raw_stream(dev))
+    return _elsewhere("w8a8_matmul", _matmul8, dev, stream, (Xq, x_scale, Wq, w_scale, group, bias, Y, dtype))
 
 
 def w4a8_quantize_weights(W, group, Wq=None, w_scale=None, w_zero=None, stream=None):

@@ -141,9 +141,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
 }
 
-// Sums and maxima over the warps of a row.  Each call has its own buffer of
-// 32 floats: a buffer is written again only after another call's barrier,
-// which every thread passes after it has read the first one.
+// Sums and maxima over the warps of a row.  A buffer is not written again
+// before another call's barrier, which every thread passes after it has read
+// this one.
 __device__ __forceinline__ float row_sum(float v, float* buf, int nwarps) {
   v = warp_sum(v);
   if (nwarps == 1) return v;
@@ -203,58 +203,37 @@ __device__ __forceinline__ uint32_t pack_bytes4(uint32_t t0, uint32_t t1, uint32
   return __byte_perm(__byte_perm(t0, t1, 0x0040), __byte_perm(t2, t3, 0x0040), 0x5410);
 }
 
-// Codes of 8 elements by the quotient itself.
-__device__ __noinline__ uint2 quantize8_exact(float2 f0, float2 f1, float2 f2, float2 f3, float s) {
-  const float2 f[4] = {f0, f1, f2, f3};
-  uint32_t t[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    t[j] = (uint32_t)min(max(__float2int_rn(__fdiv_rn(j & 1 ? f[j >> 1].y : f[j >> 1].x, s)), -127), 127);
-  return make_uint2(pack_bytes4(t[0], t[1], t[2], t[3]), pack_bytes4(t[4], t[5], t[6], t[7]));
-}
-
-// Codes of 8 elements.  1 / s (one ulp off at most) moved by 2^-21 either way
-// brackets the IEEE quotient, whose rounding and the move's are 2^-24 each, and
-// adding 1.5 * 2^23 in one fused operation rounds to the integer: where both
-// ends agree the quotient rounds there too.  `bad` gathers disagreement (one
-// element in some 35,000), for which the quotient is taken.
-__device__ __forceinline__ uint2 quantize8(const float2 (&f)[4], float inv_lo, float inv_hi, uint32_t& bad) {
-  const float2 mg = make_float2(kMagic, kMagic), ih = make_float2(inv_hi, inv_hi), il = make_float2(inv_lo, inv_lo);
+// Codes of 8 elements: each times 1 / s (`inv`), rounded to the nearest integer
+// by adding 1.5 * 2^23 in one fused operation.  A quotient within 127 * 2^-22 of
+// a half may go to the other side; y itself is known no better than that.
+__device__ __forceinline__ uint2 quantize8(const float2 (&f)[4], float inv) {
+  const float2 mg = make_float2(kMagic, kMagic), iv = make_float2(inv, inv);
   uint32_t t[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 a = __ffma2_rn(f[j], ih, mg), b = __ffma2_rn(f[j], il, mg);
+    const float2 a = __ffma2_rn(f[j], iv, mg);
     t[2 * j] = __float_as_uint(a.x);
     t[2 * j + 1] = __float_as_uint(a.y);
-    bad |= (t[2 * j] ^ __float_as_uint(b.x)) | (t[2 * j + 1] ^ __float_as_uint(b.y));
   }
   return make_uint2(pack_bytes4(t[0], t[1], t[2], t[3]), pack_bytes4(t[4], t[5], t[6], t[7]));
 }
 
-// silu(a) b = a b (a >= 0 ? 1 : t) / (1 + t) with t = exp(-|a|) <= 1, so that
-// nothing overflows before the result does.  t = 2^p (1 + e ln 2), where p is
-// -|a| log2(e) rounded and e what the rounding left out (an exact fused
-// residual, and log2(e)'s own low part): the argument's rounding would cost
-// |a| 2^-24 of t otherwise.  Errors of t: 2 ulp of ex2.approx and 2 roundings;
-// of the rest: 1 + t, 1 ulp of rcp.approx, 3 products.
+// silu(a) b = a b / (1 + 2^(-a log2 e)).  With u = 2^-24: the exponent's two
+// roundings put 1.5 |a| u into the power and ex2.approx 4 u, of which the share
+// t / (1 + t) reaches the result (all of it for a far below 0, at most 0.3 |a| u
+// above); 1 + t, rcp.approx and two products add 5 u.  Below a = -87 the power
+// or its reciprocal leaves fp32's range and the result is 0 (exactly: under
+// 1.2e-36 |b|).
 __device__ __forceinline__ float2 silu_mul2(float2 a, float2 b) {
-  constexpr float kLog2e = 1.4426950408889634f, kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
-  constexpr float kLn2 = 0.6931471805599453f;
-  const float2 x = make_float2(-fabsf(a.x), -fabsf(a.y));
-  const float2 l = make_float2(kLog2e, kLog2e), ll = make_float2(kLog2eLow, kLog2eLow), ln2 = make_float2(kLn2, kLn2);
-  const float2 p = __fmul2_rn(x, l);
-  const float2 np = make_float2(-p.x, -p.y);
-  const float2 e = __ffma2_rn(x, ll, __ffma2_rn(x, l, np));
-  float2 t0;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(t0.x) : "f"(p.x));
-  asm("ex2.approx.f32 %0, %1;" : "=f"(t0.y) : "f"(p.y));
-  const float2 t = __ffma2_rn(__fmul2_rn(t0, e), ln2, t0);
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float2 p = __fmul2_rn(a, make_float2(-kLog2e, -kLog2e));
+  float2 t, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(t.x) : "f"(p.x));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(t.y) : "f"(p.y));
   const float2 d = __fadd2_rn(t, make_float2(1.0f, 1.0f));
-  float2 r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
-  const float2 g = make_float2(a.x >= 0.0f ? 1.0f : t.x, a.y >= 0.0f ? 1.0f : t.y);
-  return __fmul2_rn(__fmul2_rn(__fmul2_rn(a, r), g), b);
+  return __fmul2_rn(__fmul2_rn(a, r), b);
 }
 
 // How far into a row an element at e is: 8 or more where every chunk is whole.
@@ -263,115 +242,145 @@ __device__ __forceinline__ int left(int K, int e) {
   return FULL ? 8 : K - e;
 }
 
-// A row whose 8 VPT elements per thread are in f: for OP 0 the sum before the
-// norm, for OP 1 the gated product.  FULL: every thread has all of its chunks
-// inside the row.  gamma(v, g) gives the weights of chunk v; taken() runs in
-// every thread once all of the row's threads have their inputs in registers.
-template <class T, int OP, int VPT, bool VEC, bool FULL, class Gamma, class Taken>
-__device__ __forceinline__ void finish_row(float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t, int tpr,
-                                           int nwarps, float (*red)[32], Gamma&& gamma, Taken&& taken) {
-  using W = typename T::word;
-  const int lane = threadIdx.x & 31;
-  if constexpr (OP == 0) {
-    if (p.H) {
-      W* h = static_cast<W*>(p.H) + row * p.ldh;
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int e = (v * tpr + t) * 8;
-        store8<T, VEC>(h + e, left<FULL>(p.K, e), f[v]);
-      }
-    }
-    float2 s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(f[v][j], f[v][j], s2);
-    float ss = row_sum(__fadd_rn(s2.x, s2.y), red[0], nwarps);
-    taken();
-    float eps = p.eps;
-    if (!(ss <= 3.4e38f)) {   // the same value in every thread of the row
-      float m = 0.0f;
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = max_abs(m, f[v][j]);
-      m = row_max(m, red[2], nwarps);
-      // an infinity or a NaN stays one through all that follows
-      const float k = m < __int_as_float(0x7F800000) ? exp2f(1.0f - (float)ilogbf(m)) : 1.0f;
-      s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[v][j].x *= k;
-          f[v][j].y *= k;
-          s2 = __ffma2_rn(f[v][j], f[v][j], s2);
-        }
-      ss = row_sum(__fadd_rn(s2.x, s2.y), red[0], nwarps);
-      eps = eps * k * k;
-    }
-    // 1 / sqrt(x): the hardware's estimate (2 ulp) and one Newton step
-    const float x = fmaf(ss, p.inv_k, eps);
-    float r;
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    r = fmaf(0.5f * r, fmaf(-x * r, r, 1.0f), r);
-    const float2 r2 = make_float2(r, r);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], r2);
-      if (p.gamma) {
-        float2 g[4];
-        gamma(v, g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], g[j]);
-      }
-    }
-  }
-  if (p.group) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) rotate8(f[v], p.group, lane);
-  }
+template <int VPT>
+__device__ __forceinline__ float thread_max(const float2 (&f)[VPT][4]) {
   float m = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
 #pragma unroll
     for (int j = 0; j < 4; ++j) m = max_abs(m, f[v][j]);
-  m = row_max(m, red[1], nwarps);
-  if constexpr (OP == 1) taken();
+  return m;
+}
+template <int VPT>
+__device__ __forceinline__ float thread_squares(const float2 (&f)[VPT][4]) {
+  float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(f[v][j], f[v][j], s2);
+  return __fadd_rn(s2.x, s2.y);
+}
+template <int VPT>
+__device__ __forceinline__ void scale_row(float2 (&f)[VPT][4], float k) {
+  const float2 k2 = make_float2(k, k);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], k2);
+}
+
+// 1 / sqrt(x): the hardware's estimate (2 ulp) and one Newton step
+__device__ __forceinline__ float inv_sqrt(float x) {
+  float r;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return fmaf(0.5f * r, fmaf(-x * r, r, 1.0f), r);
+}
+
+struct RowShared {
+  float sum[32], max[2][32];
+};
+
+template <class T, int VPT, bool VEC, bool FULL>
+__device__ __forceinline__ void store_sum(const float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t,
+                                          int tpr) {
+  if (!p.H) return;
+  auto* h = static_cast<typename T::word*>(p.H) + row * p.ldh;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = (v * tpr + t) * 8;
+    store8<T, VEC>(h + e, left<FULL>(p.K, e), f[v]);
+  }
+}
+template <int VPT>
+__device__ __forceinline__ void rotate_row(float2 (&f)[VPT][4], int group) {
+  if (group) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) rotate8(f[v], group, (int)threadIdx.x & 31);
+  }
+}
+// Scale and codes of a row y in f whose max |y| is m.
+template <int VPT, bool VEC, bool FULL>
+__device__ __forceinline__ void quantize_row(float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t, int tpr,
+                                             float m) {
   const bool finite = m < __int_as_float(0x7F800000);
   const float s = finite ? __fdiv_rn(m, 127.0f) : __int_as_float(0x7FC00000);
   if (t == 0) p.x_scale[row] = s;
-  // Codes are 0 in a row of zeros and in one whose scale is NaN; a scale too
-  // small for its reciprocal takes the quotients.
-  const bool some = s > 0.0f, tiny = s < 0x1p-100f;
+  // Codes are 0 in a row of zeros and in one whose scale is NaN.
+  const bool some = s > 0.0f;
   const uint32_t keep = some ? 0xFFFFFFFFu : 0u;
   float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(tiny || !some ? 1.0f : s));
-  const float inv_hi = __fmul_rn(inv, 1.0f + 0x1p-21f), inv_lo = __fmul_rn(inv, 1.0f - 0x1p-21f);
-  uint32_t bad = tiny ? 1u : 0u;
-  uint2 w[VPT];
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(some && s >= 0x1p-100f ? s : 1.0f));
+  if (some && s < 0x1p-100f) {     // too small for its reciprocal, and of few bits itself where it is subnormal
+    scale_row(f, 0x1p80f);
+    const float big = s * 0x1p80f, top = 127.0f * big;
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) w[v] = quantize8(f[v], inv_lo, inv_hi, bad);
-  if (bad & keep) {
+    for (int v = 0; v < VPT; ++v)
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) w[v] = quantize8_exact(f[v][0], f[v][1], f[v][2], f[v][3], s);
+      for (int j = 0; j < 4; ++j)
+        f[v][j] = make_float2(fminf(fmaxf(f[v][j].x, -top), top), fminf(fmaxf(f[v][j].y, -top), top));
+    inv = __frcp_rn(big);
   }
   int8_t* q = p.Xq + row * p.ldq;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int e = (v * tpr + t) * 8;
     const int n = left<FULL>(p.K, e);
-    w[v].x &= keep;
-    w[v].y &= keep;
+    uint2 w = quantize8(f[v], inv);
+    w.x &= keep;
+    w.y &= keep;
     if (FULL || n >= 8) {
-      *reinterpret_cast<uint2*>(q + e) = w[v];
+      *reinterpret_cast<uint2*>(q + e) = w;
     } else if (!VEC) {
 #pragma unroll
       for (int j = 0; j < 7; ++j)
-        if (j < n) q[e + j] = (int8_t)((j < 4 ? w[v].x >> (8 * j) : w[v].y >> (8 * j - 32)) & 0xFFu);
+        if (j < n) q[e + j] = (int8_t)((j < 4 ? w.x >> (8 * j) : w.y >> (8 * j - 32)) & 0xFFu);
     }
   }
+}
+
+// The norm of a row h in f, its rotation, scale and codes: a reduction for the
+// sum of squares and one for max |y|, and two more with h scaled by a power of two
+// where the squares pass fp32's range.  gamma(v, g) gives the weights of chunk
+// v; taken() runs in every thread once all have their inputs in registers.
+template <int VPT, bool VEC, bool FULL, class Gamma, class Taken>
+__device__ __forceinline__ void norm_row(float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t, int tpr,
+                                         RowShared& sh, Gamma&& gamma, Taken&& taken) {
+  const int nwarps = tpr >> 5;
+  float eps = p.eps;
+  float ss = row_sum(thread_squares(f), sh.sum, nwarps);
+  taken();
+  if (!(ss <= 3.4e38f)) {          // the same value in every thread of the row
+    const float m = row_max(thread_max(f), sh.max[1], nwarps);
+    // an infinity or a NaN stays one through all that follows
+    const float k = m < __int_as_float(0x7F800000) ? exp2f(1.0f - (float)ilogbf(m)) : 1.0f;
+    scale_row(f, k);
+    ss = row_sum(thread_squares(f), sh.sum, nwarps);
+    eps = eps * k * k;
+  }
+  scale_row(f, inv_sqrt(fmaf(ss, p.inv_k, eps)));
+  if (p.gamma) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      float2 g[4];
+      gamma(v, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], g[j]);
+    }
+  }
+  rotate_row(f, p.group);
+  const float m = row_max(thread_max(f), sh.max[0], nwarps);
+  quantize_row<VPT, VEC, FULL>(f, p, row, t, tpr, m);
+}
+
+// The rotation, scale and codes of a row y in f: one reduction, so rows
+// alternate between two buffers.
+template <int VPT, bool VEC, bool FULL, class Taken>
+__device__ __forceinline__ void plain_row(float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t, int tpr,
+                                          float* buf, Taken&& taken) {
+  rotate_row(f, p.group);
+  const float m = row_max(thread_max(f), buf, tpr >> 5);
+  taken();
+  quantize_row<VPT, VEC, FULL>(f, p, row, t, tpr, m);
 }
 
 // The second operand into f: added (OP 0) or gated by it (OP 1).
@@ -384,35 +393,40 @@ __device__ __forceinline__ void combine8(float2 (&f)[4], const float2 (&g)[4]) {
 // OP 0: norm (A = x, B = residual or null, gamma, H or null); OP 1: silu (A =
 // gate, B = up).  VPT: chunks of 8 per thread.  Rows straight from global
 // memory: few rows, rows off the 16-byte alignment (VEC false), rows whose
-// inputs do not fit in shared memory.
+// inputs do not fit in shared memory.  One row per team of tpr threads.
 template <class T, int OP, int VPT, int MAXT, bool VEC>
 __global__ void __launch_bounds__(MAXT) row_quantize_kernel(RowQuantArgs p, int tpr) {
   using W = typename T::word;
-  __shared__ float red[3][32];
+  __shared__ RowShared sh;
   const int rpb = blockDim.x / tpr;            // > 1 only where a row is one warp
   const int t = threadIdx.x % tpr;
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr; row < p.M; row += (int64_t)gridDim.x * rpb) {
-    const W* a = static_cast<const W*>(p.A) + row * p.lda;
-    const W* b = p.B ? static_cast<const W*>(p.B) + row * p.ldb : nullptr;
-    float2 f[VPT][4];
+  const int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+  if (row >= p.M) return;
+  const W* a = static_cast<const W*>(p.A) + row * p.lda;
+  const W* b = p.B ? static_cast<const W*>(p.B) + row * p.ldb : nullptr;
+  float2 f[VPT][4];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = (v * tpr + t) * 8;
+    load8<T, VEC>(a + e, p.K - e, f[v]);
+  }
+  if (b) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int e = (v * tpr + t) * 8;
-      load8<T, VEC>(a + e, p.K - e, f[v]);
+      float2 g[4];
+      load8<T, VEC>(b + e, p.K - e, g);
+      combine8<OP>(f[v], g);
     }
-    if (b) {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int e = (v * tpr + t) * 8;
-        float2 g[4];
-        load8<T, VEC>(b + e, p.K - e, g);
-        combine8<OP>(f[v], g);
-      }
-    }
-    finish_row<T, OP, VPT, VEC, false>(
-        f, p, row, t, tpr, tpr >> 5, red,
+  }
+  if constexpr (OP == 1) {
+    plain_row<VPT, VEC, false>(f, p, row, t, tpr, sh.max[0], [] {});
+  } else {
+    store_sum<T, VPT, VEC, false>(f, p, row, t, tpr);
+    norm_row<VPT, VEC, false>(
+        f, p, row, t, tpr, sh,
         [&](int v, float2 (&g)[4]) {
           const int e = (v * tpr + t) * 8;
           load8<T, VEC>(static_cast<const W*>(p.gamma) + e, p.K - e, g);
@@ -448,6 +462,22 @@ __device__ __forceinline__ void smem8(uint32_t addr, int n, float2 (&f)[4]) {
   }
 }
 
+// The inputs of a row in shared memory, combined.
+template <class T, int OP, int VPT, bool FULL>
+__device__ __forceinline__ void read_row(float2 (&f)[VPT][4], uint32_t src, uint32_t row_bytes, const RowQuantArgs& p,
+                                         int t, int tpr) {
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = (v * tpr + t) * 8;
+    const uint32_t at = src + (uint32_t)(e * sizeof(typename T::word));
+    smem8<T>(at, left<FULL>(p.K, e), f[v]);
+    if (p.B) {
+      float2 g[4];
+      smem8<T>(at + row_bytes, left<FULL>(p.K, e), g);
+      combine8<OP>(f[v], g);
+    }
+  }
+}
 // Many aligned rows: persistent blocks, each row's inputs brought into a ring
 // of `stages` rows in shared memory by bulk copies, so that the next rows
 // arrive while one is worked on and no register holds a load in flight.  A
@@ -462,7 +492,7 @@ __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAX
   // the weights of a thread's elements stay in registers, packed, where they fit
   constexpr bool kHoldGamma = OP == 0 && T::kWords == 4 && MAXT < 1024;
   extern __shared__ __align__(128) uint8_t ring_raw[];
-  __shared__ float red[3][32];
+  __shared__ RowShared sh;
   __shared__ __align__(8) uint64_t full[kRingTeams][kRingStages];
   const int rpb = blockDim.x / tpr;
   const int team = threadIdx.x / tpr, t = threadIdx.x % tpr;
@@ -495,43 +525,40 @@ __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAX
                                      : make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  int s = 0;
+  int s = 0, parity = 0;
   uint32_t ph = 0;
-  for (int64_t row = row0; row < p.M; row += step) {
+  for (int64_t row = row0; row < p.M; row += step, parity ^= 1) {
     if (!mbar_wait(&full[team][s], ph)) set_device_error(err, kDevErrTimeoutFull);
     const uint32_t src = ring + (uint32_t)s * stage_bytes;
     float2 f[VPT][4];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int e = (v * tpr + t) * 8;
-      smem8<T>(src + (uint32_t)e * sizeof(W), left<FULL>(p.K, e), f[v]);
-      if (p.B) {
-        float2 g[4];
-        smem8<T>(src + row_bytes + (uint32_t)e * sizeof(W), left<FULL>(p.K, e), g);
-        combine8<OP>(f[v], g);
-      }
-    }
+    read_row<T, OP, VPT, FULL>(f, src, row_bytes, p, t, tpr);
     // the row's sum or maximum depends on everything that its threads read
     // here, so once it is known the stage takes the row after next
-    finish_row<T, OP, VPT, true, FULL>(
-        f, p, row, t, tpr, tpr >> 5, red,
-        [&](int v, float2 (&g)[4]) {
-          if constexpr (kHoldGamma) {
-            g[0] = T::two(gw[v].x);
-            g[1] = T::two(gw[v].y);
-            g[2] = T::two(gw[v].z);
-            g[3] = T::two(gw[v].w);
-          } else {
-            const int e = (v * tpr + t) * 8;
-            load8<T, true>(static_cast<const W*>(p.gamma) + e, left<FULL>(p.K, e), g);
-          }
-        },
-        [&] {
-          if (t == 0 && row + stages * step < p.M) {
-            fence_proxy_async_smem();
-            issue(row + stages * step, s);
-          }
-        });
+    auto taken = [&] {
+      if (t == 0 && row + stages * step < p.M) {
+        fence_proxy_async_smem();
+        issue(row + stages * step, s);
+      }
+    };
+    if constexpr (OP == 1) {
+      plain_row<VPT, true, FULL>(f, p, row, t, tpr, sh.max[parity], taken);
+    } else {
+      store_sum<T, VPT, true, FULL>(f, p, row, t, tpr);
+      norm_row<VPT, true, FULL>(
+          f, p, row, t, tpr, sh,
+          [&](int v, float2 (&g)[4]) {
+            if constexpr (kHoldGamma) {
+              g[0] = T::two(gw[v].x);
+              g[1] = T::two(gw[v].y);
+              g[2] = T::two(gw[v].z);
+              g[3] = T::two(gw[v].w);
+            } else {
+              const int e = (v * tpr + t) * 8;
+              load8<T, true>(static_cast<const W*>(p.gamma) + e, left<FULL>(p.K, e), g);
+            }
+          },
+          taken);
+    }
     if (++s == stages) {
       s = 0;
       ph ^= 1u;
@@ -571,7 +598,10 @@ cudaError_t launch_direct(const RowQuantArgs& a, int vpt, cudaStream_t st) {
   return launch_rows(row_quantize_kernel<T, OP, 4, 1024, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
 }
 
-constexpr int kRingBytes = 200 * 1024;     // of an SM's shared memory
+// An SM's shared memory for rings: 228 KB less 2 KB for each block (the runtime's
+// share and the static variables).
+constexpr int kSmemSm = 228 * 1024, kSmemBlock = 2 * 1024;
+constexpr int kRingMax = 224 * 1024;
 
 struct RingPlan {
   int vpt, tpr, rpb, stages, per_sm;
@@ -586,9 +616,10 @@ bool plan_ring(int K, size_t stage, RingPlan& pl) {
   if (chunks > 4 * 384) vpt = chunks <= 1024 * 2 ? 2 : 4;
   const int tpr = threads_per_row(chunks, vpt);
   const int rpb = tpr == 32 ? kRingTeams : 1;
-  const int per_sm = (int)std::min<size_t>(kRingBytes / (2 * stage * rpb), std::max(1, kRingThreads / (tpr * rpb)));
-  if (per_sm < 1) return false;
-  pl = RingPlan{vpt, tpr, rpb, (int)std::min<size_t>(kRingStages, kRingBytes / (stage * rpb * per_sm)), per_sm};
+  const int per_sm = (int)std::min<size_t>(kSmemSm / (2 * stage * rpb + kSmemBlock), std::max(1, kRingThreads / (tpr * rpb)));
+  if (per_sm < 1 || 2 * stage * rpb > kRingMax) return false;
+  const size_t room = std::min<size_t>(kSmemSm / per_sm - kSmemBlock, kRingMax);
+  pl = RingPlan{vpt, tpr, rpb, (int)std::min<size_t>(kRingStages, room / (stage * rpb)), per_sm};
   return true;
 }
 
@@ -598,7 +629,7 @@ cudaError_t launch_ring_t(const RowQuantArgs& a, const RingPlan& pl, size_t stag
   static DeviceFlags configured;
   cudaError_t e;
   if (!configured.done(dev)) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingMax)) != cudaSuccess) return e;
     configured.set(dev);
   }
   unsigned int* err = device_error_word();
