@@ -194,6 +194,9 @@ SHAPES = [
     (6, 192, 64, 8, 8), (5, 256, 128, 0, 0), (7, 257, 0, 0, 0), (13, 640, 128, 5, 3), (3, 1000, 0, 0, 0),
     (2, 1031, 0, 0, 1), (700, 264, 0, 0, 0), (601, 384, 64, 1, 0), (333, 1024, 128, 0, 0), (320, 2304, 0, 24, 0),
     (1, 4096, 128, 0, 0), (310, 4096, 0, 0, 0), (2, 8192, 64, 0, 0), (300, 8200, 0, 0, 0), (299, 16384, 128, 0, 0),
+    (700, 9, 0, 0, 0), (900, 13, 0, 0, 1), (640, 8, 0, 1, 0), (701, 257, 0, 0, 0), (400, 1031, 0, 3, 1),
+    (350, 2777, 0, 0, 0), (333, 8191, 0, 0, 0), (320, 5461, 0, 1, 5), (500, 128, 128, 1, 1), (1500, 300, 0, 2, 3),
+    (2000, 1029, 0, 0, 0), (600, 12289, 0, 0, 0), (400, 264, 0, 1, 0), (400, 4100, 0, 0, 7),
     (1, 20001, 0, 0, 0), (3, 32768, 128, 0, 0), (300, 32768, 0, 0, 0), (301, 32767, 0, 0, 0),
 ]
 
@@ -205,7 +208,7 @@ def test_norm(M, K, group, pad, offset, dtype):
     import torch
     dt = _dt(dtype)
     X = _rows(_data(M, K, 1), dt, pad, offset)
-    R = _rows(_data(M, K, 2, 2.0), dt, 0, offset) if (M + K) % 3 else None
+    R = _rows(_data(M, K, 2, 2.0), dt, K % 4, offset) if (M + K) % 3 else None
     gamma = _rows(1 + 0.1 * _data(1, K, 3), dt, 0, offset)[0] if K % 5 else None
     if M > 4:
         X[3] = 0                       # a padding row
@@ -213,7 +216,12 @@ def test_norm(M, K, group, pad, offset, dtype):
             R[3] = 0
     ldq = (K + 15) // 16 * 16 + 16
     buf = torch.full((M + 1, ldq), 99, dtype=torch.int8, device="cuda")
-    q, s, h = w4.w8a8_add_rmsnorm_quantize(X, gamma, EPS, group, residual=R, Xq=buf[:M, :K])
+    H, hbuf = None, None
+    if R is not None:                  # rows of H at an offset and a stride of their own
+        ldh = K + (M % 5)
+        hbuf = torch.full((M * ldh + 9,), 5.0, dtype=dt, device="cuda")
+        H = hbuf.as_strided((M, K), (ldh, 1), M % 7)
+    q, s, h = w4.w8a8_add_rmsnorm_quantize(X, gamma, EPS, group, residual=R, H=H, Xq=buf[:M, :K])
     torch.cuda.synchronize()
     h64, y64 = norm64(_f64(X), None if R is None else _f64(R), None if gamma is None else _f64(gamma), EPS)
     check_codes(y64, group, 21, _f64(q), _f64(s))
@@ -223,6 +231,9 @@ def test_norm(M, K, group, pad, offset, dtype):
     else:
         half = torch.finfo(dt).eps / 2
         tiny = 2.0 ** -25 if dtype == "fp16" else 0.0             # half a step below fp16's normal range
+        rest = hbuf.clone()
+        rest.as_strided((M, K), (ldh, 1), M % 7).fill_(5.0)
+        assert (rest == 5.0).all()                                # nothing between the rows or around them
         assert np.all(np.abs(_f64(h) - h64) <= (half + 2 * U) * np.abs(h64) + tiny)
 
 
@@ -357,11 +368,11 @@ def test_weights_of_extreme_size(M, group):
 
 
 @gpu
-@pytest.mark.parametrize("K", [63, 2048])
-def test_sum_in_place_of_an_input(K):
+@pytest.mark.parametrize("M,K", [(40, 63), (40, 2048), (1000, 63), (1000, 2048), (2000, 1025)])
+def test_sum_in_place_of_an_input(M, K):
     import torch
     for which in ("X", "residual"):
-        X, R = _rows(_data(40, K, 7), torch.bfloat16), _rows(_data(40, K, 8), torch.bfloat16)
+        X, R = _rows(_data(M, K, 7), torch.bfloat16), _rows(_data(M, K, 8), torch.bfloat16)
         q, s, h = w4.w8a8_add_rmsnorm_quantize(X.clone(), None, EPS, residual=R.clone())
         into = X if which == "X" else R
         q2, s2, h2 = w4.w8a8_add_rmsnorm_quantize(X, None, EPS, residual=R, H=into)

@@ -462,42 +462,175 @@ __device__ __forceinline__ void smem8(uint32_t addr, int n, float2 (&f)[4]) {
   }
 }
 
-// The inputs of a row in shared memory, combined.
-template <class T, int OP, int VPT, bool FULL>
-__device__ __forceinline__ void read_row(float2 (&f)[VPT][4], uint32_t src, uint32_t row_bytes, const RowQuantArgs& p,
-                                         int t, int tpr) {
+// How the rows of a ring lie: every thread has whole chunks (kWhole), the last
+// threads may have none (kAligned), or rows start off the 16-byte alignment or
+// end inside a chunk (kShifted).
+enum RowLayout { kWhole, kAligned, kShifted };
+
+// Words i0 .. i0 + n - 1 of a window, moved down by `bytes` (0 to 15, the same in
+// the whole block).
+template <int IN, int OUT>
+__device__ __forceinline__ void shift_words(const uint32_t (&w)[IN], uint32_t bytes, uint32_t (&out)[OUT]) {
+  static_assert(IN >= OUT + 4, "a window of one 16-byte granule more");
+  const uint32_t bits = (bytes & 3u) * 8u;
+  switch (bytes >> 2) {
+    case 0:
 #pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int e = (v * tpr + t) * 8;
-    const uint32_t at = src + (uint32_t)(e * sizeof(typename T::word));
-    smem8<T>(at, left<FULL>(p.K, e), f[v]);
-    if (p.B) {
-      float2 g[4];
-      smem8<T>(at + row_bytes, left<FULL>(p.K, e), g);
-      combine8<OP>(f[v], g);
+      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], bits);
+      break;
+    case 1:
+#pragma unroll
+      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 1], w[i + 2], bits);
+      break;
+    case 2:
+#pragma unroll
+      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 2], w[i + 3], bits);
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 3], i + 4 < IN ? w[i + 4] : 0u, bits);
+  }
+}
+
+// The first n of 8 elements whose row begins `off` bytes into a 16-byte granule
+// of shared memory; the rest are zero.  at: the granule that the first one lies
+// in once `off` is added (the same `off` for every chunk of a row).
+template <class T>
+__device__ __forceinline__ void smem8_shifted(uint32_t at, uint32_t off, int n, float2 (&f)[4]) {
+  constexpr int NW = T::kWords;
+  uint32_t w[NW + 4], u[NW];
+#pragma unroll
+  for (int i = 0; i < NW / 4 + 1; ++i) {
+    w[4 * i] = w[4 * i + 1] = w[4 * i + 2] = w[4 * i + 3] = 0u;
+    if (n > 0)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(at + 16 * i));
+  }
+  shift_words(w, off, u);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (NW == 4) f[j] = T::two(u[j]);
+    else f[j] = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+  }
+  if (n < 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (2 * j >= n) f[j].x = 0.0f;
+      if (2 * j + 1 >= n) f[j].y = 0.0f;
     }
   }
 }
-// Many aligned rows: persistent blocks, each row's inputs brought into a ring
-// of `stages` rows in shared memory by bulk copies, so that the next rows
-// arrive while one is worked on and no register holds a load in flight.  A
-// team of tpr threads owns a ring; with rows of one warp a block has several.
+
+// A row of the sum to global memory at any element alignment.  A whole chunk's
+// thread writes the 16-byte granules that begin in it, filling the first with
+// the end of the chunk before, which the lane below holds; what no such thread
+// covers (the first bytes of a warp's first chunk, the last bytes before a warp
+// or the row ends, a partial chunk) goes element by element.
+template <class T, int VPT>
+__device__ __forceinline__ void store_sum_shifted(const float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t,
+                                                  int tpr) {
+  using W = typename T::word;
+  constexpr int NW = T::kWords;
+  if (!p.H) return;
+  W* h = static_cast<W*>(p.H) + row * p.ldh;
+  const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(h) & 15u);
+  const int own = (int)((16u - off) / sizeof(W));       // elements of a chunk before its first granule begins
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = (v * tpr + t) * 8;
+    const int n = p.K - e;
+    uint32_t u[NW], w[NW + 4], g[NW];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (NW == 4) {
+        u[j] = T::pack(f[v][j]);
+      } else {
+        u[2 * j] = __float_as_uint(f[v][j].x);
+        u[2 * j + 1] = __float_as_uint(f[v][j].y);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __shfl_up_sync(0xFFFFFFFFu, u[NW - 4 + j], 1);
+#pragma unroll
+    for (int j = 0; j < NW; ++j) w[4 + j] = u[j];
+    int lo = 0, hi = 0;                                  // elements [0, lo) and [hi, 8) are written one by one
+    if (off == 0) {
+      if (n >= 8) {
+#pragma unroll
+        for (int q = 0; q < NW / 4; ++q)
+          reinterpret_cast<uint4*>(h + e)[q] = make_uint4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+        hi = 8;
+      } else {
+        lo = max(n, 0);
+        hi = 8;
+      }
+    } else if (n < 8) {
+      lo = max(n, 0);
+      hi = 8;
+    } else {
+      // granules at h + e - off: the first holds the lane below's last `off` bytes
+      shift_words(w, 16u - off, g);
+      uint4* at = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(h + e) - off);
+#pragma unroll
+      for (int q = 0; q < NW / 4; ++q)
+        if (q > 0 || lane > 0) at[q] = make_uint4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]);
+      lo = lane > 0 ? 0 : own;
+      hi = lane == 31 || n < 16 ? 8 - (int)(off / sizeof(W)) : 8;   // nobody's granule takes the end
+    }
+    if (lo > 0 || hi < 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < lo || i >= hi) {
+          if constexpr (NW == 4) h[e + i] = (W)((i & 1) ? u[i / 2] >> 16 : u[i / 2] & 0xFFFFu);
+          else h[e + i] = u[i];
+        }
+    }
+  }
+}
+
+// Where an operand's row lies in its slot of a stage: the bytes from the 16-byte
+// granule of its first element to that of its last.
+struct RowSpan {
+  const uint8_t* from;
+  uint32_t off, bytes;
+};
+__device__ __forceinline__ RowSpan row_span(const void* row, uint32_t row_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(row);
+  const uint32_t off = (uint32_t)(a & 15u);
+  return RowSpan{reinterpret_cast<const uint8_t*>(a - off), off, (off + row_bytes + 15u) & ~15u};
+}
+// A slot holds any such span and the granule past it that a window may touch.
+__host__ __device__ __forceinline__ uint32_t slot_bytes(uint32_t row_bytes, bool shifted) {
+  return shifted ? ((row_bytes + 15u) & ~15u) + 32u : row_bytes;
+}
+
+// Many rows: persistent blocks, each row's inputs brought into a ring of
+// `stages` rows in shared memory by bulk copies, so that the next rows arrive
+// while one is worked on and no register holds a load in flight.  A team of tpr
+// threads owns a ring; with rows of one warp a block has several.  kShifted
+// copies whole 16-byte granules, so a row brings up to 14 bytes of its
+// neighbours along; the first and the last row, which have none on one side,
+// are read from global memory element by element.
 constexpr int kRingStages = 4, kRingTeams = 4;
 constexpr int kRingThreads = 768;          // threads of an SM (1024 where rows are too wide for fewer)
 
-template <class T, int OP, int VPT, int MAXT, bool FULL>
+template <class T, int OP, int VPT, int MAXT, RowLayout LAY>
 __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAXT : 1)
     row_ring_kernel(RowQuantArgs p, int tpr, int stages, unsigned int* err) {
   using W = typename T::word;
+  constexpr bool FULL = LAY == kWhole;
   // the weights of a thread's elements stay in registers, packed, where they fit
-  constexpr bool kHoldGamma = OP == 0 && T::kWords == 4 && MAXT < 1024;
+  constexpr bool kHoldGamma = OP == 0 && T::kWords == 4 && MAXT < 1024 && LAY != kShifted;
   extern __shared__ __align__(128) uint8_t ring_raw[];
   __shared__ RowShared sh;
   __shared__ __align__(8) uint64_t full[kRingTeams][kRingStages];
   const int rpb = blockDim.x / tpr;
   const int team = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const uint32_t row_bytes = (uint32_t)p.K * sizeof(W);
-  const uint32_t stage_bytes = p.B ? 2 * row_bytes : row_bytes;
+  const uint32_t slot = slot_bytes(row_bytes, LAY == kShifted);
+  const uint32_t stage_bytes = p.B ? 2 * slot : slot;
   const uint32_t ring = smem_u32(ring_raw) + (uint32_t)(team * stages) * stage_bytes;
   const int64_t row0 = (int64_t)blockIdx.x * rpb + team, step = (int64_t)gridDim.x * rpb;
   if (t == 0) {
@@ -507,11 +640,25 @@ __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAX
   __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
+  auto a_row = [&](int64_t row) { return static_cast<const W*>(p.A) + row * p.lda; };
+  auto b_row = [&](int64_t row) { return static_cast<const W*>(p.B) + row * p.ldb; };
+  auto at_end = [&](int64_t row) { return LAY == kShifted && (row == 0 || row == p.M - 1); };
   auto issue = [&](int64_t row, int s) {
-    mbar_arrive_expect_tx(&full[team][s], stage_bytes);
+    if (at_end(row)) {
+      mbar_arrive(&full[team][s]);
+      return;
+    }
     const uint32_t dst = ring + (uint32_t)s * stage_bytes;
-    bulk_load(dst, static_cast<const W*>(p.A) + row * p.lda, row_bytes, &full[team][s]);
-    if (p.B) bulk_load(dst + row_bytes, static_cast<const W*>(p.B) + row * p.ldb, row_bytes, &full[team][s]);
+    if constexpr (LAY == kShifted) {
+      const RowSpan a = row_span(a_row(row), row_bytes), b = row_span(p.B ? b_row(row) : a_row(row), row_bytes);
+      mbar_arrive_expect_tx(&full[team][s], a.bytes + (p.B ? b.bytes : 0u));
+      bulk_load(dst, a.from, a.bytes, &full[team][s]);
+      if (p.B) bulk_load(dst + slot, b.from, b.bytes, &full[team][s]);
+    } else {
+      mbar_arrive_expect_tx(&full[team][s], stage_bytes);
+      bulk_load(dst, a_row(row), row_bytes, &full[team][s]);
+      if (p.B) bulk_load(dst + slot, b_row(row), row_bytes, &full[team][s]);
+    }
   };
   if (t == 0)
     for (int s = 0; s < stages; ++s)
@@ -531,7 +678,29 @@ __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAX
     if (!mbar_wait(&full[team][s], ph)) set_device_error(err, kDevErrTimeoutFull);
     const uint32_t src = ring + (uint32_t)s * stage_bytes;
     float2 f[VPT][4];
-    read_row<T, OP, VPT, FULL>(f, src, row_bytes, p, t, tpr);
+    const bool direct = at_end(row);
+    const uint32_t oa = LAY == kShifted ? (uint32_t)(reinterpret_cast<uintptr_t>(a_row(row)) & 15u) : 0u;
+    const uint32_t ob = LAY == kShifted && p.B ? (uint32_t)(reinterpret_cast<uintptr_t>(b_row(row)) & 15u) : 0u;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int e = (v * tpr + t) * 8;
+      const int n = left<FULL>(p.K, e);
+      const uint32_t at = src + (uint32_t)(e * sizeof(W));
+      float2 g[4];
+      if constexpr (LAY == kShifted) {
+        if (direct) {
+          load8<T, false>(a_row(row) + e, n, f[v]);
+          if (p.B) load8<T, false>(b_row(row) + e, n, g);
+        } else {
+          smem8_shifted<T>(at, oa, n, f[v]);
+          if (p.B) smem8_shifted<T>(at + slot, ob, n, g);
+        }
+      } else {
+        smem8<T>(at, n, f[v]);
+        if (p.B) smem8<T>(at + slot, n, g);
+      }
+      if (p.B) combine8<OP>(f[v], g);
+    }
     // the row's sum or maximum depends on everything that its threads read
     // here, so once it is known the stage takes the row after next
     auto taken = [&] {
@@ -541,10 +710,11 @@ __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAX
       }
     };
     if constexpr (OP == 1) {
-      plain_row<VPT, true, FULL>(f, p, row, t, tpr, sh.max[parity], taken);
+      plain_row<VPT, LAY != kShifted, FULL>(f, p, row, t, tpr, sh.max[parity], taken);
     } else {
-      store_sum<T, VPT, true, FULL>(f, p, row, t, tpr);
-      norm_row<VPT, true, FULL>(
+      if constexpr (LAY == kShifted) store_sum_shifted<T, VPT>(f, p, row, t, tpr);
+      else store_sum<T, VPT, true, FULL>(f, p, row, t, tpr);
+      norm_row<VPT, LAY != kShifted, FULL>(
           f, p, row, t, tpr, sh,
           [&](int v, float2 (&g)[4]) {
             if constexpr (kHoldGamma) {
@@ -554,7 +724,10 @@ __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAX
               g[3] = T::two(gw[v].w);
             } else {
               const int e = (v * tpr + t) * 8;
-              load8<T, true>(static_cast<const W*>(p.gamma) + e, left<FULL>(p.K, e), g);
+              const W* w = static_cast<const W*>(p.gamma) + e;
+              const int n = left<FULL>(p.K, e);
+              if (LAY != kShifted || (n >= 8 && (reinterpret_cast<uintptr_t>(p.gamma) & 15u) == 0)) load8<T, true>(w, n, g);
+              else load8<T, false>(w, n, g);
             }
           },
           taken);
@@ -611,7 +784,7 @@ struct RingPlan {
 // per thread where 384 threads then cover the row (a thread's share of the two
 // reductions is some 120 instructions), else the fewest that 1024 threads allow.
 bool plan_ring(int K, size_t stage, RingPlan& pl) {
-  const int chunks = K / 8;
+  const int chunks = (K + 7) / 8;
   int vpt = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
   if (chunks > 4 * 384) vpt = chunks <= 1024 * 2 ? 2 : 4;
   const int tpr = threads_per_row(chunks, vpt);
@@ -623,9 +796,9 @@ bool plan_ring(int K, size_t stage, RingPlan& pl) {
   return true;
 }
 
-template <class T, int OP, int VPT, int MAXT, bool FULL>
+template <class T, int OP, int VPT, int MAXT, RowLayout LAY>
 cudaError_t launch_ring_t(const RowQuantArgs& a, const RingPlan& pl, size_t stage, int sms, int dev, cudaStream_t st) {
-  auto kern = row_ring_kernel<T, OP, VPT, MAXT, FULL>;
+  auto kern = row_ring_kernel<T, OP, VPT, MAXT, LAY>;
   static DeviceFlags configured;
   cudaError_t e;
   if (!configured.done(dev)) {
@@ -640,9 +813,11 @@ cudaError_t launch_ring_t(const RowQuantArgs& a, const RingPlan& pl, size_t stag
 }
 
 template <class T, int OP, int VPT, int MAXT>
-cudaError_t launch_ring(const RowQuantArgs& a, const RingPlan& pl, size_t stage, int sms, int dev, cudaStream_t st) {
-  return a.K == 8 * VPT * pl.tpr ? launch_ring_t<T, OP, VPT, MAXT, true>(a, pl, stage, sms, dev, st)
-                                 : launch_ring_t<T, OP, VPT, MAXT, false>(a, pl, stage, sms, dev, st);
+cudaError_t launch_ring(const RowQuantArgs& a, const RingPlan& pl, bool vec, size_t stage, int sms, int dev,
+                        cudaStream_t st) {
+  if (!vec) return launch_ring_t<T, OP, VPT, MAXT, kShifted>(a, pl, stage, sms, dev, st);
+  if (a.K == 8 * VPT * pl.tpr) return launch_ring_t<T, OP, VPT, MAXT, kWhole>(a, pl, stage, sms, dev, st);
+  return launch_ring_t<T, OP, VPT, MAXT, kAligned>(a, pl, stage, sms, dev, st);
 }
 
 template <class T, int OP>
@@ -656,17 +831,19 @@ cudaError_t launch_op(const RowQuantArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
-  // Few rows (at most two per SM): a chunk per thread, the shortest chain.
-  const int vpt = a.M <= 2 * sms ? 1 : 4;
-  if (!vec) return launch_direct<T, OP, false>(a, vpt, st);
+  // Few rows (at most two per SM): a chunk per thread, the shortest chain.  Rows
+  // under 16 bytes have no granule of their own to copy.
   RingPlan pl;
-  const size_t stage = (size_t)a.K * es * (a.B ? 2 : 1);
-  if (a.M <= 2 * sms || !plan_ring(a.K, stage, pl)) return launch_direct<T, OP, true>(a, vpt, st);
-  if (pl.vpt == 1) return launch_ring<T, OP, 1, 384>(a, pl, stage, sms, dev, st);
-  if (pl.vpt == 2 && pl.tpr <= 384) return launch_ring<T, OP, 2, 384>(a, pl, stage, sms, dev, st);
-  if (pl.vpt == 2) return launch_ring<T, OP, 2, 1024>(a, pl, stage, sms, dev, st);
-  if (pl.tpr <= 384) return launch_ring<T, OP, 4, 384>(a, pl, stage, sms, dev, st);
-  return launch_ring<T, OP, 4, 1024>(a, pl, stage, sms, dev, st);
+  const size_t stage = (size_t)slot_bytes((uint32_t)(a.K * es), !vec) * (a.B ? 2 : 1);
+  if (a.M <= 2 * sms || a.K * es < 16 || !plan_ring(a.K, stage, pl)) {
+    const int vpt = a.M <= 2 * sms ? 1 : 4;
+    return vec ? launch_direct<T, OP, true>(a, vpt, st) : launch_direct<T, OP, false>(a, vpt, st);
+  }
+  if (pl.vpt == 1) return launch_ring<T, OP, 1, 384>(a, pl, vec, stage, sms, dev, st);
+  if (pl.vpt == 2 && pl.tpr <= 384) return launch_ring<T, OP, 2, 384>(a, pl, vec, stage, sms, dev, st);
+  if (pl.vpt == 2) return launch_ring<T, OP, 2, 1024>(a, pl, vec, stage, sms, dev, st);
+  if (pl.tpr <= 384) return launch_ring<T, OP, 4, 384>(a, pl, vec, stage, sms, dev, st);
+  return launch_ring<T, OP, 4, 1024>(a, pl, vec, stage, sms, dev, st);
 }
 
 template <class T>
