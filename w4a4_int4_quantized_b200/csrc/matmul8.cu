@@ -292,7 +292,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
-  grid_dependency_wait();
 
   // This pair's tiles and k-blocks.
   const int64_t tiles = (int64_t)pl.tiles_m * pl.tiles_n;
@@ -308,6 +307,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else {
     t0 = blockIdx.x >> 1;
     tstep = gridDim.x >> 1;
+  }
+
+  // The next kernel of the stream may start where this one leaves SMs free, and
+  // a split asks the first weights into L2 before it waits for the previous
+  // kernel (a hint: the loads after the wait read memory as it then is).  256 x
+  // 4096 x 12288 in thirds: 20.2 -> 19.7 -> 19.5 us; 333 x 1013 x 2995: 10.0 -> 9.4.
+  if (SPLIT && warp == 3 && lane == 0) {
+    int tm, tn;
+    tile_at(t0, pl, tm, tn);
+    for (int kb = kb0; kb < min(kb1, kb0 + 4); ++kb)
+      prefetch_tile_l2(&tmB, kb * BK, tn * BN + (int)half * C::kBRows);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // SPLIT: this thread's columns in the final sum, their scales and bias loaded
+  // while the products run
+  constexpr int kG = SPLIT ? BN / 128 : 1;             // groups of four columns per lane
+  int64_t sm0 = 0, sn0 = 0;
+  float ssw[kG][4], sbs[kG][4];
+  if constexpr (SPLIT) {
+    int tm, tn;
+    tile_at(t0, pl, tm, tn);
+    sm0 = (int64_t)tm * 2 * BM + (int64_t)half * BM;
+    sn0 = (int64_t)tn * BN + lane * 4;
+#pragma unroll
+    for (int c = 0; c < kG; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t n = sn0 + c * 128 + j;
+        const auto* bias = static_cast<const typename O::elem*>(p.bias);
+        ssw[c][j] = n < p.N ? p.b_scale[n] : 0.0f;
+        sbs[c][j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
+      }
   }
 
   if (warp == 0) {
@@ -502,54 +535,51 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   cluster_sync();
   if constexpr (SPLIT) {
     // Rows r = q, q + S, ... of this CTA's 128: the pairs' partials summed, a
-    // lane per four columns.
-    constexpr int kG = BN / 128;                     // groups of four columns per lane
-    int tm, tn;
-    tile_at(t0, pl, tm, tn);
-    const int64_t m0 = (int64_t)tm * 2 * BM + (int64_t)half * BM;
-    const int64_t n0 = (int64_t)tn * BN + lane * 4;
+    // lane per four columns.  128 columns keep two rows of remote loads in flight
+    // (256 x 4096 x 12288 in halves 22.4 -> 21.3 us); 256 columns are bound by the
+    // SM-to-SM network (2.4 TB/s) and gain nothing from it.
+    constexpr int kRows = BN == 128 ? 2 : 1;
+    const int64_t m0 = sm0, n0 = sn0;
     const int S = pl.split;
-    float sw[kG][4], bs[kG][4];
-#pragma unroll
-    for (int c = 0; c < kG; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t n = n0 + c * 128 + j;
-        const auto* bias = static_cast<const typename O::elem*>(p.bias);
-        sw[c][j] = n < p.N ? p.b_scale[n] : 0.0f;
-        bs[c][j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
-      }
+    const int step = (kTileThreads / 32) * S;
     uint32_t peer[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) peer[q] = map_to_rank(base, (uint32_t)(2 * (q < S ? q : 0)) + half);
-    for (int r = (int)(crank >> 1) + warp * S; r < BM; r += (kTileThreads / 32) * S) {
-      const int64_t m = m0 + r;
-      if (m >= p.M) break;
-      const float s = p.a_scale[m];
-      uint4 v[4][kG];
+    for (int r = (int)(crank >> 1) + warp * S; r < BM && m0 + r < p.M; r += kRows * step) {
+      const bool two = kRows == 2 && r + step < BM && m0 + r + step < p.M;
+      const float sx[2] = {p.a_scale[m0 + r], two ? p.a_scale[m0 + r + step] : 0.0f};
+      uint4 v[kRows][4][kG];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int c = 0; c < kG; ++c)
-          if (q < S) v[q][c] = ld_cluster_v4(peer[q] + (uint32_t)(r * C::kPartPitch + (c * 128 + lane * 4) * 4));
-#pragma unroll
-      for (int c = 0; c < kG; ++c) {
-        int a[4] = {0, 0, 0, 0};
+      for (int h = 0; h < kRows; ++h)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (q < S) {
-            a[0] += (int)v[q][c].x;
-            a[1] += (int)v[q][c].y;
-            a[2] += (int)v[q][c].z;
-            a[3] += (int)v[q][c].w;
-          }
-        const int64_t n = n0 + c * 128;
-        if (n >= p.N) continue;
-        const bool hb = p.bias != nullptr;
-        float y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], s, sw[c][j], p.inv_group, bs[c][j], hb);
-        store4<O>(static_cast<typename O::elem*>(p.Y) + m * p.ldy + n, (int)min((int64_t)4, p.N - n), p.vec_out, y);
+          for (int c = 0; c < kG; ++c)
+            if (q < S && (h == 0 || two))
+              v[h][q][c] = ld_cluster_v4(peer[q] + (uint32_t)((r + h * step) * C::kPartPitch + (c * 128 + lane * 4) * 4));
+#pragma unroll
+      for (int h = 0; h < kRows; ++h) {
+        if (h == 1 && !two) break;
+#pragma unroll
+        for (int c = 0; c < kG; ++c) {
+          int a[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < S) {
+              a[0] += (int)v[h][q][c].x;
+              a[1] += (int)v[h][q][c].y;
+              a[2] += (int)v[h][q][c].z;
+              a[3] += (int)v[h][q][c].w;
+            }
+          const int64_t n = n0 + c * 128;
+          if (n >= p.N) continue;
+          const bool hb = p.bias != nullptr;
+          float y[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], sx[h], ssw[c][j], p.inv_group, sbs[c][j], hb);
+          store4<O>(static_cast<typename O::elem*>(p.Y) + (m0 + r + h * step) * p.ldy + n, (int)min((int64_t)4, p.N - n),
+                    p.vec_out, y);
+        }
       }
     }
     cluster_sync();                                  // the partials stay readable until every CTA has summed
@@ -910,9 +940,9 @@ cudaError_t launch_streamed(const Matmul8Args& a, int sms, int dev, cudaStream_t
 
 // Tile width and K slices of the pair kernel by a model of its time in us: a
 // k-block costs 0.26 (256 x 128) or 0.30 (256 x 256) once its operands stream,
-// a launch 7 to 9 with its first loads and last epilogue, a split 1.5 for its
+// a launch 6 to 8 with its first loads and last epilogue, a split 1.5 for its
 // cluster barriers and sum; whole tiles walk in rounds of SMs / 2.  M = 256, K =
-// 12288, N = 4096: 37.7 whole at 256 wide, 24.0 in halves, 20.7 in thirds, 22.4 in
+// 12288, N = 4096: 37.6 whole at 256 wide, 24.0 in halves, 19.5 in thirds, 21.3 in
 // halves at 128 wide; clusters of 8 that are not all resident cost a second
 // round (34.4).
 template <class O>
@@ -924,7 +954,7 @@ cudaError_t launch_tiled(const Matmul8Args& a, int sms, int dev, cudaStream_t st
   int bn = 256, split = 1;
   for (int w : {256, 128}) {
     const int64_t tiles = (int64_t)tiles_m * (((int64_t)a.N + w - 1) / w);
-    const float kb = w == 256 ? 0.30f : 0.26f, base = w == 256 ? 9.0f : 7.0f;
+    const float kb = w == 256 ? 0.30f : 0.26f, base = w == 256 ? 8.0f : 6.0f;
     for (int s = 1; s <= 4; ++s) {
       if (s > 1 && (tiles * s > pairs || nk < 2 * s)) break;
       if (s > 1 && tiles > (w == 256 ? resident_tiles<256, O>(s, dev) : resident_tiles<128, O>(s, dev))) continue;
