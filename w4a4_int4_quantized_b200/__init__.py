@@ -258,42 +258,34 @@ def w8a8_linear(X, Wq, w_scale, group, bias=None, Y=None, workspace=None, stream
 
 # ---- around the INT8 product: strided rows, three element types -------------
 #
-# A decoded token's kernels take 2 to 6 us, so what these functions do before
-# the launch is kept short: the common case (tensors of the current device, its
-# current stream) goes straight to the C call, with no context managers and
-# the raw stream handle.
+# A decoded token's kernels take 2 to 6 us, so what happens before the launch is
+# kept short: the tensors are checked and the C function is called in _calls.so,
+# and the common case (tensors of the current device, its current stream) needs
+# no context manager and no stream object.
 
-_torch = _dtypes = _raw_stream = _cur_device = None
+_torch = _calls = _raw_stream = _cur_device = None
 
 
-def _bind_torch():
-    global _torch, _dtypes, _raw_stream, _cur_device
+def _bind_calls():
+    """Load _calls.so and give it the library's entry points."""
+    global _torch, _calls, _raw_stream, _cur_device
+    import importlib.machinery
+    import importlib.util
+
     import torch
-    load_library()
-    _dtypes = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    lib = load_library()
+    path = os.path.join(_HERE, "_calls.so")
+    if not os.path.exists(path):
+        raise W4A4Error("load_library", 4) from FileNotFoundError(
+            f"{path} not built; run __graft_entry__.build() or python -m w4a4_int4_quantized_b200.build")
+    loader = importlib.machinery.ExtensionFileLoader(__name__ + "._calls", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(__name__ + "._calls", path,
+                                                                                    loader=loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                  for f in (lib.w8a8_add_rmsnorm_quantize, lib.w8a8_silu_mul_quantize, lib.w8a8_matmul)))
     _raw_stream, _cur_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _torch = torch
-
-
-def _matrix(fn, t, shape, dtype, dev):
-    """Data pointer and row stride (in elements) of a matrix whose rows are
-    contiguous; refuses another shape (M, K), element type or device."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        raise W4A4Error(fn, 1)
-    if t.shape != shape:
-        raise W4A4Error(fn, 2)
-    ld, one = t.stride()
-    if one != 1 and shape[1] != 1:
-        raise W4A4Error(fn, 2)
-    return t.data_ptr(), ld
-
-
-def _vector(fn, t, n, dtype, dev):
-    if t.dtype is not dtype or t.get_device() != dev:
-        raise W4A4Error(fn, 1)
-    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
-        raise W4A4Error(fn, 2)
-    return t.data_ptr()
+    _torch, _calls = torch, module
 
 
 def _codes_out(M, K, like):
@@ -302,45 +294,30 @@ def _codes_out(M, K, like):
 
 
 def _elsewhere(fn, core, dev, stream, args):
-    """core(*args) off the common path: tensors of another device than the
-    current one, or a stream that was given; outputs that core allocates belong
-    to the stream that it launches on."""
+    """core(*args, raw stream) off the common path: tensors of another device
+    than the current one, or a stream that was given; outputs that core
+    allocates belong to the stream that it launches on."""
     if dev < 0:
         raise W4A4Error(fn, 6)
     if stream is None:
         with _torch.cuda.device(dev):
-            return core(*args, dev, _raw_stream(dev))
+            return core(*args, _raw_stream(dev))
     if stream.device.index != dev:
         raise W4A4Error(fn, 1)
     with _torch.cuda.stream(stream):
-        return core(*args, dev, stream.cuda_stream)
+        return core(*args, stream.cuda_stream)
 
 
-def _add_rmsnorm_quantize(X, gamma, eps, group, residual, H, Xq, x_scale, dev, st):
-    fn = "w8a8_add_rmsnorm_quantize"
-    dt = X.dtype
-    shape = M, K = X.shape
-    x, ldx = _matrix(fn, X, shape, dt, dev)
-    r = g = h = None
-    ldr = ldh = 0
-    if residual is not None:
-        r, ldr = _matrix(fn, residual, shape, dt, dev)
-        if H is None:
-            H = _torch.empty((M, K), dtype=dt, device=X.device)
-    if gamma is not None:
-        g = _vector(fn, gamma, K, dt, dev)
-    if H is not None:
-        h, ldh = _matrix(fn, H, shape, dt, dev)
+def _add_rmsnorm_quantize(X, gamma, eps, group, residual, H, Xq, x_scale, st):
+    if H is None and residual is not None:
+        H = _torch.empty(X.shape, dtype=X.dtype, device=X.device)
     if Xq is None:
-        Xq = _codes_out(M, K, X)
+        Xq = _codes_out(*X.shape, X)
     if x_scale is None:
-        x_scale = _torch.empty((M,), dtype=_torch.float32, device=X.device)
-    q, ldq = _matrix(fn, Xq, shape, _torch.int8, dev)
-    s = _vector(fn, x_scale, M, _torch.float32, dev)
-    status = _lib.w8a8_add_rmsnorm_quantize(x, ldx, r, ldr, g, eps, M, K, group, _dtypes.get(dt, -1), h, ldh, q, ldq,
-                                            s, st)
+        x_scale = _torch.empty(X.shape[:1], dtype=_torch.float32, device=X.device)
+    status = _calls.add_rmsnorm_quantize(X, gamma, eps, group, residual, H, Xq, x_scale, st)
     if status:
-        raise W4A4Error(fn, status)
+        raise W4A4Error("w8a8_add_rmsnorm_quantize", status)
     return Xq, x_scale, H
 
 
@@ -351,30 +328,23 @@ def w8a8_add_rmsnorm_quantize(X, gamma, eps, group=0, residual=None, H=None, Xq=
     (X + residual rounded to the type) is allocated when there is a residual
     and None otherwise; it may be X or residual itself.  Codes allocated here
     have their rows 16-byte aligned (a stride of K rounded up)."""
-    if _torch is None:
-        _bind_torch()
+    if _calls is None:
+        _bind_calls()
     dev = X.get_device()
     if stream is None and dev >= 0 and dev == _cur_device():
-        return _add_rmsnorm_quantize(X, gamma, eps, group, residual, H, Xq, x_scale, dev, _raw_stream(dev))
+        return _add_rmsnorm_quantize(X, gamma, eps, group, residual, H, Xq, x_scale, _raw_stream(dev))
     return _elsewhere("w8a8_add_rmsnorm_quantize", _add_rmsnorm_quantize, dev, stream,
                       (X, gamma, eps, group, residual, H, Xq, x_scale))
 
 
-def _silu_mul_quantize(gate, up, group, Xq, x_scale, dev, st):
-    fn = "w8a8_silu_mul_quantize"
-    dt = gate.dtype
-    shape = M, K = gate.shape
-    a, lda = _matrix(fn, gate, shape, dt, dev)
-    b, ldb = _matrix(fn, up, shape, dt, dev)
+def _silu_mul_quantize(gate, up, group, Xq, x_scale, st):
     if Xq is None:
-        Xq = _codes_out(M, K, gate)
+        Xq = _codes_out(*gate.shape, gate)
     if x_scale is None:
-        x_scale = _torch.empty((M,), dtype=_torch.float32, device=gate.device)
-    q, ldq = _matrix(fn, Xq, shape, _torch.int8, dev)
-    s = _vector(fn, x_scale, M, _torch.float32, dev)
-    status = _lib.w8a8_silu_mul_quantize(a, lda, b, ldb, M, K, group, _dtypes.get(dt, -1), q, ldq, s, st)
+        x_scale = _torch.empty(gate.shape[:1], dtype=_torch.float32, device=gate.device)
+    status = _calls.silu_mul_quantize(gate, up, group, Xq, x_scale, st)
     if status:
-        raise W4A4Error(fn, status)
+        raise W4A4Error("w8a8_silu_mul_quantize", status)
     return Xq, x_scale
 
 
@@ -382,32 +352,22 @@ def w8a8_silu_mul_quantize(gate, up, group=0, Xq=None, x_scale=None, stream=None
     """SiLU(gate) * up, rotation and per-token int8 quantization in one kernel:
     (codes [M, K], scales [M]).  gate and up are bf16, fp16 or fp32 [M, K],
     rows of any stride: the halves of one [M, 2 K] product need no copy."""
-    if _torch is None:
-        _bind_torch()
+    if _calls is None:
+        _bind_calls()
     dev = gate.get_device()
     if stream is None and dev >= 0 and dev == _cur_device():
-        return _silu_mul_quantize(gate, up, group, Xq, x_scale, dev, _raw_stream(dev))
+        return _silu_mul_quantize(gate, up, group, Xq, x_scale, _raw_stream(dev))
     return _elsewhere("w8a8_silu_mul_quantize", _silu_mul_quantize, dev, stream, (gate, up, group, Xq, x_scale))
 
 
-def _matmul8(Xq, x_scale, Wq, w_scale, group, bias, Y, dtype, dev, st):
-    fn = "w8a8_matmul"
-    M, K = Xq.shape
-    N = Wq.shape[0]
-    i8, f32 = _torch.int8, _torch.float32
-    a, lda = _matrix(fn, Xq, (M, K), i8, dev)
-    b, ldb = _matrix(fn, Wq, (N, K), i8, dev)
-    sa, sb = _vector(fn, x_scale, M, f32, dev), _vector(fn, w_scale, N, f32, dev)
+def _matmul8(Xq, x_scale, Wq, w_scale, group, bias, Y, dtype, st):
     if Y is None:
-        Y = _torch.empty((M, N), dtype=dtype or _torch.bfloat16, device=Xq.device)
-    dt = Y.dtype
-    if dtype is not None and dtype is not dt:
-        raise W4A4Error(fn, 1)
-    v = None if bias is None else _vector(fn, bias, N, dt, dev)
-    y, ldy = _matrix(fn, Y, (M, N), dt, dev)
-    status = _lib.w8a8_matmul(a, lda, sa, b, ldb, sb, M, N, K, group, v, _dtypes.get(dt, -1), y, ldy, st)
+        Y = _torch.empty((Xq.shape[0], Wq.shape[0]), dtype=dtype or _torch.bfloat16, device=Xq.device)
+    elif dtype is not None and dtype is not Y.dtype:
+        raise W4A4Error("w8a8_matmul", 1)
+    status = _calls.matmul(Xq, x_scale, Wq, w_scale, group, bias, Y, st)
     if status:
-        raise W4A4Error(fn, status)
+        raise W4A4Error("w8a8_matmul", status)
     return Y
 
 
@@ -416,12 +376,13 @@ def w8a8_matmul(Xq, x_scale, Wq, w_scale, group=0, bias=None, Y=None, dtype=None
     ((Xq Wq^T * x_scale) * w_scale) / group + bias in bf16, fp16 or fp32 (the
     type of Y, else `dtype`, else bf16; the bias is of the same type).  Code
     matrices have rows a multiple of 16 bytes apart, Y rows of any stride."""
-    if _torch is None:
-        _bind_torch()
+    if _calls is None:
+        _bind_calls()
     dev = Xq.get_device()
     if stream is None and dev >= 0 and dev == _cur_device():
-        return _matmul8(Xq, x_scale, Wq, w_scale, group, bias, Y, dtype, dev, _raw_stream(dev))
-    return _elsewhere("w8a8_matmul", _matmul8, dev, stream, (Xq, x_scale, Wq, w_scale, group, bias, Y, dtype))
+        return _matmul8(Xq, x_scale, Wq, w_scale, group, bias, Y, dtype, _raw_stream(dev))
+    return _elsewhere("w8a8_matmul", _matmul8, dev, stream,
+                      (Xq, x_scale, Wq, w_scale, group, bias, Y, dtype))
 
 
 def w4a8_quantize_weights(W, group, Wq=None, w_scale=None, w_zero=None, stream=None):

@@ -3,7 +3,8 @@
 Every translation unit under ``csrc/`` is compiled for ``sm_100a`` only (no
 PTX for other targets, no other architectures), then linked into one shared
 object next to this file, with the CUDA runtime linked statically so the
-library loads on hosts without a GPU.
+library loads on hosts without a GPU.  ``_calls.so`` beside it (``calls.cpp``,
+g++ against torch's headers) marshals the arguments of the shortest calls.
 """
 from __future__ import annotations
 
@@ -19,6 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libw4a4.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
+CALLS = os.path.join(HERE, "_calls.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
@@ -58,7 +61,30 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _build_calls(force: bool) -> None:
+    deps = [CALLS_SRC, os.path.join(INCLUDE, "w4a4.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(CALLS) and all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
+        return
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), f"-Wl,-rpath,{os.path.join(root, 'lib')}",
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    _build_calls(force)
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
