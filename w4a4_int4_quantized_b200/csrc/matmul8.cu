@@ -133,15 +133,16 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// At most 8 tokens.  Bound by the latency of one round of loads: each warp has
-// all of U * kFewWarps * 64 = 4096 codes of k in flight at once, and the
-// weights are asked into L2 before the wait for the previous kernel (a hint;
-// the loads after the wait read memory as it then is).  N = K = 4096, one
-// token, replayed back to back: 6.1 us with U = 4, 6.1 with U = 8, 5.1 with
-// the hint and U = 8 (5.6 with U = 4).
+// At most 8 tokens.  Bound by the latency of the loads: each warp has U k steps in
+// flight, and the block's weights are asked into L2 before the wait for the
+// previous kernel (a hint; the loads after the wait read memory as it then is).
+// Three blocks per SM leave room for the next kernel's blocks, whose hints then
+// run under this one.  One token, N = K = 4096, replayed back to back: 6.1 us
+// without the hint, 5.2 with it and U = 8 (two blocks per SM), 5.3 with U = 4; N =
+// 6144 9.6 and 6.0, N = 4096 with K = 1024 3.3 and 2.8.
 template <class O>
-__global__ void __launch_bounds__(kFewWarps * 32) few_tokens_kernel(Matmul8Args p) {
-  constexpr int U = 8;             // k steps (64 codes) in flight per warp
+__global__ void __launch_bounds__(kFewWarps * 32, 3) few_tokens_kernel(Matmul8Args p) {
+  constexpr int U = 4;             // k steps (64 codes) in flight per warp
   __shared__ int part[kFewWarps][8][kFewRows + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -974,10 +975,10 @@ cudaError_t launch_tiled(const Matmul8Args& a, int sms, int dev, cudaStream_t st
 
 template <class O>
 cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
-  // Up to 8 tokens and 24 MB of weights every load fits in flight at once (16.8
-  // MB: 5.1 us against 7.4 streamed); larger weights stream (58.7 MB: 18.5
-  // against 13.3).
-  if (a.M <= 8 && (int64_t)a.N * a.K <= (int64_t)24 << 20) return launch_few<O>(a, st);
+  // Up to 8 tokens, 24 MB of weights and 8192 codes of k: 25 MB 6.0 us against 9.6
+  // streamed, 34 MB 10.4 against 9.7; N = 1024 with K = 4096 3.7 against 5.0, with K
+  // = 16384 12.0 against 8.8.
+  if (a.M <= 8 && a.K <= 8192 && (int64_t)a.N * a.K <= (int64_t)24 << 20) return launch_few<O>(a, st);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
