@@ -250,3 +250,91 @@ def test_gated_mlp(M, D, F, group, dtype):
     check_product(gu, q, s, Wgu, sgu, group, None)
     check_codes(silu64(_f64(gu[:, :F]), _f64(gu[:, F:])), group, silu_c(_f64(gu[:, :F])), _f64(q2), _f64(s2))
     check_product(Y, q2, s2, Wd, sd, group, None)
+
+
+_FIRST_CALL = """
+import sys
+import torch
+import w4a4_int4_quantized_b200 as w4
+M, D, F = (int(v) for v in sys.argv[1:4])
+g = torch.Generator(device="cuda").manual_seed(3)
+X = torch.randn((M, D), generator=g, device="cuda").to(torch.bfloat16)
+W = torch.randint(-127, 128, (2 * F, D), generator=g, device="cuda", dtype=torch.int8)
+sw = torch.rand(2 * F, generator=g, device="cuda") * 0.001
+q, s = torch.empty((M, D), dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+q2, s2 = torch.empty((M, F), dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+Y = torch.empty((M, 2 * F), dtype=torch.bfloat16, device="cuda")
+
+def block():
+    w4.w8a8_add_rmsnorm_quantize(X, None, 1e-6, Xq=q, x_scale=s)
+    w4.w8a8_matmul(q, s, W, sw, Y=Y)
+    w4.w8a8_silu_mul_quantize(Y[:, :F], Y[:, F:], Xq=q2, x_scale=s2)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    block()                      # the process's first call of each kernel
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (q, s, Y, q2, s2)]
+block()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (q, s, Y, q2, s2)))
+assert w4.w4a4_get_device_error() == 0
+print("same")
+"""
+
+
+@gpu
+@pytest.mark.parametrize("M,D,F", [(2, 512, 640), (40, 1024, 640), (300, 1024, 640), (2000, 4096, 2560)])
+def test_first_calls_of_a_process_inside_a_capture(M, D, F):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALL, str(M), str(D), str(F)], cwd=root, capture_output=True,
+                       text=True, timeout=120)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@gpu
+def test_host_threads_on_their_own_streams():
+    """Calls of all three operators from several host threads at once."""
+    import concurrent.futures as cf
+
+    import torch
+    cases = []
+    for M, D, F in ((1, 1024, 512), (20, 1024, 1536), (200, 768, 1024), (500, 2048, 512)):
+        X = _rows(_data(M, D, M), torch.bfloat16)
+        Wq, sw = _codes(2 * F, D, M + 1), torch.rand(2 * F, device="cuda") * 1e-3
+        cases.append((X, Wq, sw, F))
+
+    def run(case, stream):
+        X, Wq, sw, F = case
+        q, s, _ = w4.w8a8_add_rmsnorm_quantize(X, None, EPS, stream=stream)
+        Y = w4.w8a8_matmul(q, s, Wq, sw, stream=stream)
+        return (q, s, Y, *w4.w8a8_silu_mul_quantize(Y[:, :F], Y[:, F:], stream=stream))
+
+    want = [run(c, torch.cuda.current_stream()) for c in cases]
+    torch.cuda.synchronize()
+
+    def worker(i):
+        st = torch.cuda.Stream()
+        got = [run(cases[(i + k) % 4], st) for k in range(40)]
+        st.synchronize()
+        return all(torch.equal(a, b) for k in range(40) for a, b in zip(got[k], want[(i + k) % 4]))
+
+    with cf.ThreadPoolExecutor(4) as ex:
+        assert all(ex.map(worker, range(4)))
+
+
+@gpu
+def test_large_output_and_many_tiles():
+    """An output of more than 2^31 elements: its first, last and middle rows."""
+    import torch
+    M, N, K = 66000, 33000, 64
+    Xq, sx, Wq, sw, v = _case(M, N, K, 23, "bf16", True)
+    Y = w4.w8a8_matmul(Xq, sx, Wq, sw, 0, v)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 40), slice(32990, 33030), slice(M - 40, M)):
+        check_product(Y[rows], Xq[rows], sx[rows], Wq, sw, 0, v)
