@@ -108,12 +108,12 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// 16 codes at k0 of a row of K codes (16-byte aligned): zeros past K, nothing
-// read there.
-template <bool STREAM>
-__device__ __forceinline__ uint4 load_codes(const int8_t* row, int k0, int K, bool in) {
+// The codes that a row's last step (64 codes) has at k0: up to 16, zeros past K,
+// nothing read there.  Out of line: one warp of a block calls it, and only where
+// K is not a multiple of 64.
+__device__ __noinline__ uint4 load_last_codes(const int8_t* row, int k0, int K, bool in) {
   if (!in || k0 >= K) return make_uint4(0u, 0u, 0u, 0u);
-  if (k0 + 16 <= K) return STREAM ? ldg_stream(row + k0) : __ldg(reinterpret_cast<const uint4*>(row + k0));
+  if (k0 + 16 <= K) return ldg_stream(row + k0);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
   for (int i = 0; i < K - k0; ++i) {
     const uint32_t b = (uint32_t)(uint8_t)row[k0 + i] << (8 * (i & 3));
@@ -160,22 +160,34 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) few_tokens_kernel(Matmul8Ar
   const int8_t* w1 = p.B + (n0 + g + 8) * p.ldb;
   const int8_t* x = p.A + (int64_t)g * p.lda;
   int acc[4] = {};
-  const int steps = (p.K + 63) / 64;
+  const int steps = p.K / 64;      // whole ones
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
     uint4 a[U][2], b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      const bool go = s0 + u * kFewWarps < steps;
       const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
-      a[u][0] = load_codes<true>(w0, k0, p.K, in0);
-      a[u][1] = load_codes<true>(w1, k0, p.K, in1);
+      a[u][0] = go && in0 ? ldg_stream(w0 + k0) : zero;
+      a[u][1] = go && in1 ? ldg_stream(w1 + k0) : zero;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) b[u] = load_codes<false>(x, (s0 + u * kFewWarps) * 64 + 16 * t, p.K, inx);
+    for (int u = 0; u < U; ++u) {
+      const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
+      b[u] = s0 + u * kFewWarps < steps && inx ? __ldg(reinterpret_cast<const uint4*>(x + k0)) : zero;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       mma_s8(acc, a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u].x, b[u].y);
       mma_s8(acc, a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u].z, b[u].w);
     }
+  }
+  if (p.K % 64 != 0 && warp == steps % kFewWarps) {
+    const int k0 = steps * 64 + 16 * t;
+    const uint4 a0 = load_last_codes(w0, k0, p.K, in0), a1 = load_last_codes(w1, k0, p.K, in1);
+    const uint4 b = load_last_codes(x, k0, p.K, inx);
+    mma_s8(acc, a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+    mma_s8(acc, a0.z, a1.z, a0.w, a1.w, b.z, b.w);
   }
   part[warp][2 * t][g] = acc[0];
   part[warp][2 * t + 1][g] = acc[1];
