@@ -14,10 +14,10 @@
 //   operands see the same permutation of k, which the sum does not notice.  The
 //   warps' int32 partials meet in shared memory.
 //
-// stream_kernel       up to 128 tokens: the weights are the 128-row operand of
+// stream_kernel       few or small tiles: the weights are the 128-row operand of
 //   tcgen05.mma kind::i8 (one CTA), the tokens its N.  Both come by TMA through a
-//   ring of 108 KB, two CTAs per SM, so that the weights stream without a pause
-//   from tile to tile.  With few tiles K is split over a cluster and the int32
+//   ring of 108 KB, two CTAs per SM, so that one's weights stream while the other
+//   starts or ends.  With few tiles K is split over a cluster and the int32
 //   partials are summed through distributed shared memory.  A stage costs about
 //   180 ns of TMA delivery (100 to 110 bytes per ns and SM) plus 23 ns per
 //   product, in which the operands' shared-memory reads hold the copies up.
@@ -623,19 +623,31 @@ struct StreamCfg {
   static constexpr int kStage = kW + kX;
   static constexpr int ST = kStreamRing / kStage;
   static constexpr int kRing = ST * kStage;
-  static constexpr int kTmemCols = 2 * NT;
+  static constexpr int kTmemCols = NT < 32 ? 32 : NT;
   static constexpr int kSmem = 1024 + kRing + 1024 + NT * 4;   // alignment, ring, barriers, token scales
-  static_assert(kStreamRows * NT * 4 <= kRing, "partials fit where the ring was");
+  static constexpr int kPartPitch = kStreamRows * 4;           // a token's sums over the tile's channels
+  static_assert(ST >= 2 && ST <= 8, "barrier arrays");
+  static_assert(NT * kPartPitch <= kRing, "the sums fit where the ring was");
 };
 
 struct StreamBars {
-  uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
+  uint64_t full[8], empty[8], acc_full;
   uint32_t tmem_base;
 };
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+// One tile of 128 output channels, or (split > 1, a cluster of that many CTAs)
+// one slice of its K.  Warp 0 loads, warp 1 issues the products, warps 4 to 7
+// leave the int32 sums in shared memory as [token][channel], and then all
+// warps finish tokens in turn, a lane per four channels.
 template <int NT, class O>
 __global__ void __launch_bounds__(kStreamThreads, 2)
-    stream_kernel(const Matmul8Args p, int split, const __grid_constant__ CUtensorMap tmX,
+    stream_kernel(const Matmul8Args p, int split, int tiles_m, const __grid_constant__ CUtensorMap tmX,
                   const __grid_constant__ CUtensorMap tmW, unsigned int* err) {
   using C = StreamCfg<NT>;
   extern __shared__ uint8_t raw[];
@@ -645,16 +657,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   float* sx = reinterpret_cast<float*>(gbase + C::kRing + 1024);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = split > 1 ? (int)cluster_ctarank() : 0;
+  const int tile = (int)blockIdx.x / split / tiles_m;      // of channels; its token tiles are neighbours
+  const int m0 = (int)blockIdx.x / split % tiles_m * NT;
+  const int tokens = min(NT, p.M - m0);
+  const int nk = (p.K + BK - 1) / BK;
+  const int kb0 = (int)((int64_t)q * nk / split), kb1 = (int)((int64_t)(q + 1) * nk / split);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(&bar->full[s], 1);
       mbar_init(&bar->empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&bar->acc_full[b], 1);
-      mbar_init(&bar->acc_empty[b], 4);
-    }
+    mbar_init(&bar->acc_full, 1);
     fence_mbar_init();
     prefetch_tmap(&tmX);
     prefetch_tmap(&tmW);
@@ -665,34 +679,26 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (threadIdx.x < NT) sx[threadIdx.x] = (int)threadIdx.x < p.M ? p.a_scale[threadIdx.x] : 0.0f;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
 
-  const int tiles = (p.N + kStreamRows - 1) / kStreamRows;
-  const int nk = (p.K + BK - 1) / BK;
-  const int t0 = (int)blockIdx.x / split, tstep = split > 1 ? tiles : (int)gridDim.x;
-  const int kb0 = (int)((int64_t)q * nk / split), kb1 = (int)((int64_t)(q + 1) * nk / split);
-
   if (warp == 0) {
     if (lane == 0) {
-      int g = 0;
       bool ok = true;
-      for (int t = t0; t < tiles && ok; t += tstep) {
-        for (int kb = kb0; kb < kb1; ++kb, ++g) {
-          const int s = g % C::ST;
-          if (g >= C::ST && !mbar_wait(&bar->empty[s], (uint32_t)(g / C::ST - 1) & 1u)) {
-            set_device_error(err, kDevErrTimeoutEmpty);
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&bar->full[s], (uint32_t)C::kStage);
-          const uint32_t dst = base + (uint32_t)(s * C::kStage);
-          tma_load_2d(dst, &tmW, kb * BK, t * kStreamRows, &bar->full[s]);
-          tma_load_2d(dst + C::kW, &tmX, kb * BK, 0, &bar->full[s]);
+      int g = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++g) {
+        const int s = g % C::ST;
+        if (g >= C::ST && !mbar_wait(&bar->empty[s], (uint32_t)(g / C::ST - 1) & 1u)) {
+          set_device_error(err, kDevErrTimeoutEmpty);
+          ok = false;
+          break;
         }
+        mbar_arrive_expect_tx(&bar->full[s], (uint32_t)C::kStage);
+        const uint32_t dst = base + (uint32_t)(s * C::kStage);
+        tma_load_2d(dst, &tmW, kb * BK, tile * kStreamRows, &bar->full[s]);
+        tma_load_2d(dst + C::kW, &tmX, kb * BK, m0, &bar->full[s]);
       }
       for (int s = 0; s < C::ST && ok; ++s) {          // no copy or product is in flight any more
         const int uses = (g - s + C::ST - 1) / C::ST;
@@ -707,107 +713,105 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_i8(kStreamRows, NT);
       const uint64_t da0 = smem_desc_kmajor_sw128(base), db0 = smem_desc_kmajor_sw128(base + C::kW);
-      int s = 0, i = 0;
+      int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = t0; t < tiles && ok; t += tstep, ++i) {
-        const int b = i & 1;
-        if (i >= 2 && !mbar_wait(&bar->acc_empty[b], (uint32_t)(i / 2 - 1) & 1u)) {
-          set_device_error(err, kDevErrTimeoutAcc);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&bar->full[s], ph)) {
+          set_device_error(err, kDevErrTimeoutFull);
+          ok = false;
           break;
         }
-        tc_fence_after();
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&bar->full[s], ph)) {
-            set_device_error(err, kDevErrTimeoutFull);
-            ok = false;
-            break;
-          }
-          const uint64_t off = (uint64_t)(s * (C::kStage >> 4));   // descriptors count 16 bytes
+        const uint64_t off = (uint64_t)(s * (C::kStage >> 4));   // descriptors count 16 bytes
 #pragma unroll
-          for (int ks = 0; ks < BK / 32; ++ks)
-            mma_i8_ss(tmem + (uint32_t)(b * NT), da0 + off + 2 * ks, db0 + off + 2 * ks, idesc,
-                      kb > kb0 || ks > 0 ? 1u : 0u);
-          tc_commit(&bar->empty[s]);
-          if (++s == C::ST) {
-            s = 0;
-            ph ^= 1u;
-          }
+        for (int ks = 0; ks < BK / 32; ++ks)
+          mma_i8_ss(tmem, da0 + off + 2 * ks, db0 + off + 2 * ks, idesc, kb > kb0 || ks > 0 ? 1u : 0u);
+        tc_commit(&bar->empty[s]);
+        if (++s == C::ST) {
+          s = 0;
+          ph ^= 1u;
         }
-        if (ok) tc_commit(&bar->acc_full[b]);
       }
+      if (ok) tc_commit(&bar->acc_full);
     }
     __syncwarp();
-  } else if (warp >= 4) {
-    constexpr int CH = NT < 32 ? NT : 32;
-    const int c = (warp - 4) * 32 + lane;              // this thread's channel of the tile
-    int i = 0;
-    for (int t = t0; t < tiles; t += tstep, ++i) {
-      const int b = i & 1;
-      const int64_t n = (int64_t)t * kStreamRows + c;
-      const auto* bias = static_cast<const typename O::elem*>(p.bias);
-      const float sw = n < p.N ? p.b_scale[n] : 0.0f;
-      const float bs = bias && n < p.N ? O::to(bias[n]) : 0.0f;
-      if (!mbar_wait(&bar->acc_full[b], (uint32_t)(i / 2) & 1u)) {
-        set_device_error(err, kDevErrTimeoutAcc);
-        break;
-      }
+  }
+
+  // What the final step needs from global memory, while the products run.
+  const int64_t n = (int64_t)tile * kStreamRows + 4 * lane;
+  const auto* bias = static_cast<const typename O::elem*>(p.bias);
+  float sw[4], bs[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    sw[j] = n + j < p.N ? p.b_scale[n + j] : 0.0f;
+    bs[j] = bias && n + j < p.N ? O::to(bias[n + j]) : 0.0f;
+  }
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + NT) {    // warps 2 to 5
+    const int m = (int)threadIdx.x - 64;
+    sx[m] = m < tokens ? p.a_scale[m0 + m] : 0.0f;
+  }
+  if (warp >= 4) {
+    if (mbar_wait(&bar->acc_full, 0u)) {
       tc_fence_after();
+      constexpr int CH = NT < 32 ? NT : 32;
+      const int c = (warp - 4) * 32 + lane;            // this thread's channel of the tile
 #pragma unroll
       for (int ch = 0; ch < NT / CH; ++ch) {
+        if (ch * CH >= tokens) break;
         uint32_t v[CH];
-        const uint32_t ta = tmem + ((uint32_t)((warp - 4) * 32) << 16) + (uint32_t)(b * NT + ch * CH);
+        const uint32_t ta = tmem + ((uint32_t)((warp - 4) * 32) << 16) + (uint32_t)(ch * CH);
         if constexpr (CH == 16) tmem_ld_32x32b_x16(ta, v);
         else tmem_ld_32x32b_x32(ta, v);
         tmem_wait_ld();
-        if (split > 1) {
 #pragma unroll
-          for (int j = 0; j < CH; ++j)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + (uint32_t)(((ch * CH + j) * kStreamRows + c) * 4)), "r"(v[j])
-                         : "memory");
-        } else if (n < p.N) {
-#pragma unroll
-          for (int j = 0; j < CH; ++j) {
-            const int m = ch * CH + j;
-            if (m < p.M)
-              static_cast<typename O::elem*>(p.Y)[(int64_t)m * p.ldy + n] =
-                  O::from(dequant((int)v[j], sx[m], sw, p.inv_group, bs, bias != nullptr));
-          }
-        }
+        for (int j = 0; j < CH; ++j)
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + (uint32_t)((ch * CH + j) * C::kPartPitch + c * 4)), "r"(v[j])
+                       : "memory");
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->acc_empty[b]);
+    } else {
+      set_device_error(err, kDevErrTimeoutAcc);
     }
   }
-
   tc_fence_before();
   __syncthreads();
-  if (split > 1) {
-    cluster_sync();
-    // tokens m = q, q + S, ...: a thread per channel, two tokens at a time
-    const int c = threadIdx.x & (kStreamRows - 1), half = threadIdx.x / kStreamRows;
-    const int64_t n = (int64_t)t0 * kStreamRows + c;
-    const auto* bias = static_cast<const typename O::elem*>(p.bias);
-    const float sw = n < p.N ? p.b_scale[n] : 0.0f;
-    const float bs = bias && n < p.N ? O::to(bias[n]) : 0.0f;
-    for (int m = q + half * split; m < p.M; m += 2 * split) {
-      int v[8];
+  if (split > 1) cluster_sync();
+  uint32_t peer[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        v[r] = 0;
-        if (r < split)
-          asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                       : "=r"(v[r])
-                       : "r"(map_to_rank(base, (uint32_t)r) + (uint32_t)((m * kStreamRows + c) * 4)));
-      }
-      const int acc = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-      if (n < p.N)
-        static_cast<typename O::elem*>(p.Y)[(int64_t)m * p.ldy + n] =
-            O::from(dequant(acc, sx[m], sw, p.inv_group, bs, bias != nullptr));
+  for (int r = 0; r < 8; ++r) peer[r] = split > 1 && r < split ? map_to_rank(base, (uint32_t)r) : base;
+  for (int m = q + warp * split; m < tokens; m += (kStreamThreads / 32) * split) {
+    const uint32_t at = (uint32_t)(m * C::kPartPitch + 16 * lane);
+    int a[4];
+    if (split == 1) {
+      const uint4 v = ld_shared_v4(base + at);
+      a[0] = (int)v.x;
+      a[1] = (int)v.y;
+      a[2] = (int)v.z;
+      a[3] = (int)v.w;
+    } else {
+      uint4 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < split) v[r] = ld_cluster_v4(peer[r] + at);
+      a[0] = a[1] = a[2] = a[3] = 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < split) {
+          a[0] += (int)v[r].x;
+          a[1] += (int)v[r].y;
+          a[2] += (int)v[r].z;
+          a[3] += (int)v[r].w;
+        }
     }
-    cluster_sync();                                    // the partials stay readable until every CTA has summed
+    if (n < p.N) {
+      const float s = sx[m];
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], s, sw[j], p.inv_group, bs[j], bias != nullptr);
+      store4<O>(static_cast<typename O::elem*>(p.Y) + (int64_t)(m0 + m) * p.ldy + n, (int)min((int64_t)4, p.N - n),
+                p.vec_out, y);
+    }
   }
+  if (split > 1) cluster_sync();                       // the sums stay readable until every CTA has taken them
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
@@ -816,7 +820,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 
 // ------------------------------------------------------------------ host side
 template <int NT, class O>
-cudaError_t launch_stream(const Matmul8Args& a, int split, int sms, int dev, cudaStream_t st) {
+cudaError_t launch_stream(const Matmul8Args& a, int split, int dev, cudaStream_t st) {
   using C = StreamCfg<NT>;
   auto kern = stream_kernel<NT, O>;
   static DeviceFlags configured;
@@ -831,9 +835,10 @@ cudaError_t launch_stream(const Matmul8Args& a, int split, int sms, int dev, cud
   CUtensorMap tX, tW;
   if (!codes_tmap(&tX, a.A, a.M, a.K, a.lda, NT) || !codes_tmap(&tW, a.B, a.N, a.K, a.ldb, kStreamRows))
     return cudaErrorInvalidValue;
-  const int tiles = (a.N + kStreamRows - 1) / kStreamRows;
+  const int tiles_m = (int)(((int64_t)a.M + NT - 1) / NT);
+  const int64_t tiles = ((int64_t)a.N + kStreamRows - 1) / kStreamRows * tiles_m;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min(tiles, 2 * sms)), 1, 1);
+  cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
   cfg.blockDim = dim3(kStreamThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
@@ -846,7 +851,7 @@ cudaError_t launch_stream(const Matmul8Args& a, int split, int sms, int dev, cud
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a, split, tX, tW, err);
+  return cudaLaunchKernelEx(&cfg, kern, a, split, tiles_m, tX, tW, err);
 }
 
 template <class O>
@@ -935,73 +940,87 @@ int resident_streams(int split, int dev) {
   return resident_clusters(stream_kernel<NT, O>, kStreamThreads, StreamCfg<NT>::kSmem, split, dev, cache);
 }
 
-// K slices of the streaming kernel: the fewest (1, 2, 4, 8) that give four
-// fifths of the SMs a CTA, as long as every cluster is resident at once and a
-// slice keeps two k-blocks.  16 tokens: 112 tiles (K = 4096) 13.6 us whole,
-// 15.4 in halves; 48 tiles (K = 4096) 10.0 in halves, 9.6 in quarters; 32 tiles
-// (K = 14336) 19.8 in halves, 14.3 in quarters, 14.8 in eighths.
+// A form of the product and its modelled time in us.
+struct Form {
+  int nt;        // streamed: tokens per tile; 0: pair tiles
+  int bn;        // pair tiles: their width
+  int split;
+  float cost;
+};
+
+// The streaming kernel.  A k-block costs 0.25 (16 or 32 tokens), 0.26 (64) or
+// 0.37 (128), 1.4 times that where SMs hold two CTAs, and no less than the
+// weights' way from memory; a launch 2.4 to 4 with its first loads and last
+// step; a split 0.8 for its cluster barriers and its sums' way between SMs at 3.5
+// MB per us.
 template <int NT, class O>
-cudaError_t launch_streamed(const Matmul8Args& a, int sms, int dev, cudaStream_t st) {
-  const int64_t tiles = ((int64_t)a.N + kStreamRows - 1) / kStreamRows;
+void consider_streamed(const Matmul8Args& a, int sms, int dev, Form& best) {
+  constexpr float kb = NT <= 32 ? 0.25f : NT == 64 ? 0.26f : 0.37f, base = NT <= 32 ? 2.4f : NT == 64 ? 3.0f : 4.0f;
+  const int64_t tiles = ((int64_t)a.N + kStreamRows - 1) / kStreamRows * (((int64_t)a.M + NT - 1) / NT);
   const int nk = (a.K + BK - 1) / BK;
-  int split = 1;
-  while (split < 8 && tiles * split * 5 < (int64_t)sms * 4 && nk >= 4 * split &&
-         tiles <= resident_streams<NT, O>(2 * split, dev))
-    split *= 2;
-  return launch_stream<NT, O>(a, split, sms, dev, st);
-}
-
-// Tile width and K slices of the pair kernel by a model of its time in us: a
-// k-block costs 0.26 (256 x 128) or 0.30 (256 x 256) once its operands stream,
-// a launch 6 to 8 with its first loads and last epilogue, a split 1.5 for its
-// cluster barriers and sum; whole tiles walk in rounds of SMs / 2.  M = 256, K =
-// 12288, N = 4096: 37.6 whole at 256 wide, 24.0 in halves, 19.5 in thirds, 21.3 in
-// halves at 128 wide; clusters of 8 that are not all resident cost a second
-// round (34.4).
-template <class O>
-cudaError_t launch_tiled(const Matmul8Args& a, int sms, int dev, cudaStream_t st) {
-  const int tiles_m = (int)(((int64_t)a.M + 2 * BM - 1) / (2 * BM));
-  const int nk = (a.K + BK - 1) / BK;
-  const int pairs = sms / 2;
-  float best = 1e30f;
-  int bn = 256, split = 1;
-  for (int w : {256, 128}) {
-    const int64_t tiles = (int64_t)tiles_m * (((int64_t)a.N + w - 1) / w);
-    const float kb = w == 256 ? 0.30f : 0.26f, base = w == 256 ? 8.0f : 6.0f;
-    for (int s = 1; s <= 4; ++s) {
-      if (s > 1 && (tiles * s > pairs || nk < 2 * s)) break;
-      if (s > 1 && tiles > (w == 256 ? resident_tiles<256, O>(s, dev) : resident_tiles<128, O>(s, dev))) continue;
-      const float rounds = s > 1 ? 1.0f : (float)((tiles + pairs - 1) / pairs);
-      const float cost = rounds * (float)((nk + s - 1) / s) * kb + base + (s > 1 ? 1.5f : 0.0f);
-      if (cost < best) {
-        best = cost;
-        bn = w;
-        split = s;
-      }
-    }
+  if (tiles > 0x7FFFFFFF / 8) return;
+  const float memory = (float)a.N * (float)a.K * (1.0f / 6.5e6f);
+  for (int s = 1; s <= 8; s *= 2) {
+    if (s > 1 && (nk < 2 * s || tiles * s > 2 * (int64_t)sms || tiles > resident_streams<NT, O>(s, dev))) break;
+    const int64_t ctas = tiles * s;
+    const float waves = (float)((ctas + 2 * sms - 1) / (2 * sms));
+    float cost = std::max(memory, waves * (float)((nk + s - 1) / s) * kb * (ctas > sms ? 1.4f : 1.0f)) + base;
+    if (s > 1) cost += 0.8f + (float)(ctas * NT * kStreamRows * 4 / s * (s - 1)) * (1.0f / 3.5e6f);
+    if (cost < best.cost) best = Form{NT, 0, s, cost};
   }
-  const TilePlan pl{tiles_m, (int)(((int64_t)a.N + bn - 1) / bn), split};
-  if (bn == 128) return split > 1 ? launch_tile<128, O, true>(a, pl, sms, dev, st) : launch_tile<128, O, false>(a, pl, sms, dev, st);
-  return split > 1 ? launch_tile<256, O, true>(a, pl, sms, dev, st) : launch_tile<256, O, false>(a, pl, sms, dev, st);
 }
 
+// The pair kernel.  A k-block costs 0.29 (256 x 128) or 0.30 (256 x 256), a launch
+// 4.9 or 6.5, a split 1.75; whole tiles walk in rounds of SMs / 2.  Clusters that are
+// not all resident at once would cost a second round (256 x 4096 x 12288 in
+// quarters 34 us, in thirds 19.4), so they are not considered.
+template <int BN, class O>
+void consider_tiled(const Matmul8Args& a, int sms, int dev, Form& best) {
+  constexpr float kb = BN == 256 ? 0.30f : 0.29f, base = BN == 256 ? 6.5f : 4.9f;
+  const int64_t tiles = (((int64_t)a.M + 2 * BM - 1) / (2 * BM)) * (((int64_t)a.N + BN - 1) / BN);
+  const int nk = (a.K + BK - 1) / BK, pairs = sms / 2;
+  const float memory = (float)a.N * (float)a.K * (1.0f / 6.5e6f);
+  for (int s = 1; s <= 4; ++s) {
+    if (s > 1 && (nk < 2 * s || tiles * s > pairs)) break;
+    if (s > 1 && tiles > resident_tiles<BN, O>(s, dev)) continue;
+    const float rounds = s > 1 ? 1.0f : (float)((tiles + pairs - 1) / pairs);
+    const float cost = std::max(memory, rounds * (float)((nk + s - 1) / s) * kb) + base + (s > 1 ? 1.75f : 0.0f);
+    if (cost < best.cost) best = Form{0, BN, s, cost};
+  }
+}
+
+// The form with the least modelled time.  Over 72 sizes (12 to 2000 tokens, N 200 to
+// 14336, K 500 to 12288) it is 2% above the best form measured on average, 14% at
+// most; us measured: 16 tokens, 28672 x 4096 streamed 22.1 (pair tiles 33); 64, 4096
+// x 4096 streamed in quarters 8.0 (11); 256, 1024 x 1024 streamed 5.1 (7.0); 333, 1013
+// x 2995 streamed 7.7 (9.3); 333, 4096 x 12288 pair tiles in halves 22.5 (streamed
+// 27.5); 1000, 14336 x 4096 pair tiles 51 (65).
 template <class O>
 cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
-  // Up to 8 tokens, 24 MB of weights and 8192 codes of k: 25 MB 6.0 us against 9.6
-  // streamed, 34 MB 10.4 against 9.7; N = 1024 with K = 4096 3.7 against 5.0, with K
+  // Up to 8 tokens, 24 MB of weights and 8192 codes of k: 25 MB 5.6 us against 9.6
+  // streamed, 34 MB 10.4 against 9.7; N = 1024 with K = 4096 3.0 against 4.6, with K
   // = 16384 12.0 against 8.8.
   if (a.M <= 8 && a.K <= 8192 && (int64_t)a.N * a.K <= (int64_t)24 << 20) return launch_few<O>(a, st);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
-  // Streamed weights up to 128 tokens: N = 28672, K = 4096, 128 tokens 28.9 us
-  // against 33.7 in pair tiles, N = K = 4096 11.7 against 13.9.
-  if (a.M <= 16) return launch_streamed<16, O>(a, sms, dev, st);
-  if (a.M <= 32) return launch_streamed<32, O>(a, sms, dev, st);
-  if (a.M <= 64) return launch_streamed<64, O>(a, sms, dev, st);
-  if (a.M <= 128) return launch_streamed<128, O>(a, sms, dev, st);
-  return launch_tiled<O>(a, sms, dev, st);
+  Form f{0, 0, 0, 1e30f};
+  if (a.M <= 16) consider_streamed<16, O>(a, sms, dev, f);
+  else if (a.M <= 32) consider_streamed<32, O>(a, sms, dev, f);
+  else consider_streamed<64, O>(a, sms, dev, f);
+  if (a.M > 64) consider_streamed<128, O>(a, sms, dev, f);
+  consider_tiled<256, O>(a, sms, dev, f);
+  consider_tiled<128, O>(a, sms, dev, f);
+  switch (f.nt) {
+    case 16: return launch_stream<16, O>(a, f.split, dev, st);
+    case 32: return launch_stream<32, O>(a, f.split, dev, st);
+    case 64: return launch_stream<64, O>(a, f.split, dev, st);
+    case 128: return launch_stream<128, O>(a, f.split, dev, st);
+  }
+  const TilePlan pl{(int)(((int64_t)a.M + 2 * BM - 1) / (2 * BM)), (int)(((int64_t)a.N + f.bn - 1) / f.bn), f.split};
+  if (f.bn == 128) return f.split > 1 ? launch_tile<128, O, true>(a, pl, sms, dev, st) : launch_tile<128, O, false>(a, pl, sms, dev, st);
+  return f.split > 1 ? launch_tile<256, O, true>(a, pl, sms, dev, st) : launch_tile<256, O, false>(a, pl, sms, dev, st);
 }
 
 }  // namespace
