@@ -7,6 +7,10 @@ one is given).  Functions carry the C names; outputs not passed in are
 allocated with torch before the call.  There is no CPU fallback: if the
 library is missing or a call fails, a ``W4A4Error`` is raised.
 
+The operators around the INT8 product (w8a8_add_rmsnorm_quantize,
+w8a8_silu_mul_quantize, w8a8_matmul) also take fp16 and fp32 and rows of any
+stride; their arguments are marshalled by _calls.so.
+
 bf16 tensors are torch.bfloat16; packed INT4 codes are torch.uint8 [rows, K/2];
 INT8 codes are torch.int8 [rows, K]; scales are torch.float32 [rows].
 """
