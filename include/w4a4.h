@@ -211,9 +211,11 @@ typedef enum { W4A4_DTYPE_BF16 = 0, W4A4_DTYPE_FP16 = 1, W4A4_DTYPE_FP32 = 2 } w
  *   h = X + residual (fp32; residual NULL: h = X),
  *   y = (h * (1 / sqrt(mean(h^2) + eps))) * gamma   (gamma NULL: ones),
  *   per group of `group`: y <- H_g y (group 0: none),
- *   x_scale = fl32(max |y| / 127), Xq = rint_half_even(fl32(y / x_scale)),
+ *   x_scale = fl32(max |y| / 127), Xq = rint_half_even(y / x_scale),
  * and, where H is given, H = h rounded to the type.  The norm uses the
- * unrounded h, and y is not rounded before it is quantized.
+ * unrounded h, and y is not rounded before it is quantized.  The quotient is
+ * formed with the reciprocal of x_scale in fp32: one within 127 * 2^-22 of a half
+ * may go to the other side (y itself is known to about 20 * 2^-24 of its value).
  *   X [M, K], residual [M, K] or NULL, gamma [K] or NULL, H [M, K] or NULL:
  *   `dtype`.  H may be X or residual itself (same base and stride), or share
  *   no byte with them; Xq and x_scale share no byte with any input.
@@ -226,7 +228,8 @@ w4a4_status w8a8_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* re
                                       w4a4_stream_t stream);
 
 /* SiLU(gate) * up, rotation, int8 quantization:
- *   y = (gate / (1 + exp(-gate))) * up (fp32), then as above.
+ *   y = (gate / (1 + exp(-gate))) * up (fp32), then as above.  Gates below -87
+ *   count as 0 (the function is under 1.2e-36 there).
  *   gate, up [M, K]: `dtype`; the two halves of one [M, 2 K] product are
  *   given as two pointers with the same stride.  Shapes as above. */
 w4a4_status w8a8_silu_mul_quantize(const void* gate, int64_t ldg, const void* up, int64_t ldu, int M, int K,

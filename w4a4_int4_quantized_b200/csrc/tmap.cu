@@ -38,6 +38,22 @@ struct TmapVal {
 
 }  // namespace
 
+bool encode_tmap_nd(CUtensorMap* out, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz) {
+  if (rank < 1 || rank > 3) return false;
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t gd[3], gs[2];
+  cuuint32_t bx[3], es[3] = {1, 1, 1};
+  for (int d = 0; d < rank; ++d) {
+    gd[d] = dims[d];
+    bx[d] = box[d];
+    if (d > 0) gs[d - 1] = strides_bytes[d - 1];
+  }
+  return fn(out, dt, (cuuint32_t)rank, const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_nd(CUtensorMap* out, CUtensorMapDataType dt, int esize, const void* base, int rank,
                   const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz) {
   static PlanCache<TmapKey, TmapVal, 128> cache;
@@ -52,19 +68,8 @@ bool make_tmap_nd(CUtensorMap* out, CUtensorMapDataType dt, int esize, const voi
     if (d > 0) key.v[8 + d - 1] = (int64_t)strides_bytes[d - 1];
   }
   TmapVal val;
-  const bool ok = cache.get(key, val, [&](TmapVal& v) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t gd[3], gs[2];
-    cuuint32_t bx[3], es[3] = {1, 1, 1};
-    for (int d = 0; d < rank; ++d) {
-      gd[d] = dims[d];
-      bx[d] = box[d];
-      if (d > 0) gs[d - 1] = strides_bytes[d - 1];
-    }
-    return fn(&v.map, dt, (cuuint32_t)rank, const_cast<void*>(base), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  });
+  const bool ok = cache.get(
+      key, val, [&](TmapVal& v) { return encode_tmap_nd(&v.map, dt, base, rank, dims, strides_bytes, box, swz); });
   if (ok) *out = val.map;
   return ok;
 }

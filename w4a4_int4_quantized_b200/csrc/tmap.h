@@ -13,7 +13,12 @@ namespace w4a4 {
 bool make_tmap(CUtensorMap* out, CUtensorMapDataType dt, int esize, const void* base, uint64_t rows, uint64_t cols,
                uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz);
 
-// General form: `rank` (1..3) dimensions, innermost first; strides_bytes
+// General form, encoded anew: `rank` (1..3) dimensions, innermost first;
+// strides_bytes holds the rank - 1 outer strides.
+bool encode_tmap_nd(CUtensorMap* out, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz);
+
+// The same, cached: `rank` (1..3) dimensions, innermost first; strides_bytes
 // holds the rank - 1 outer strides.
 bool make_tmap_nd(CUtensorMap* out, CUtensorMapDataType dt, int esize, const void* base, int rank,
                   const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz);
