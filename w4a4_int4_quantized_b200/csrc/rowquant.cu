@@ -786,19 +786,29 @@ struct RingPlan {
 };
 
 // Threads per row, rings and their depth for rows of `stage` bytes.  Four chunks
-// per thread where 384 threads then cover the row (a thread's share of the two
-// reductions is some 120 instructions), else the fewest that 1024 threads allow.
+// per thread (its share of the two reductions is some 120 instructions), fewer
+// where the rings that fit an SM's memory would then leave it under 512 threads
+// (norm of 8192 x 5120 fp32 96 us with 320 threads, 91 with 640) or where more than 384
+// threads hold four each in 64 registers (4096 x 16384 bf16 111 us, with two 81).
 bool plan_ring(int K, size_t stage, RingPlan& pl) {
   const int chunks = (K + 7) / 8;
-  int vpt = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
-  if (chunks > 4 * 384) vpt = chunks <= 1024 * 2 ? 2 : 4;
-  const int tpr = threads_per_row(chunks, vpt);
-  const int rpb = tpr == 32 ? kRingTeams : 1;
-  const int per_sm = (int)std::min<size_t>(kSmemSm / (2 * stage * rpb + kSmemBlock), std::max(1, kRingThreads / (tpr * rpb)));
-  if (per_sm < 1 || 2 * stage * rpb > kRingMax) return false;
-  const size_t room = std::min<size_t>(kSmemSm / per_sm - kSmemBlock, kRingMax);
-  pl = RingPlan{vpt, tpr, rpb, (int)std::min<size_t>(kRingStages, room / (stage * rpb)), per_sm};
-  return true;
+  int most = 0;
+  for (int vpt = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4; vpt >= 1; vpt /= 2) {
+    const int tpr = threads_per_row(chunks, vpt);
+    if (tpr > 1024) break;
+    if (vpt == 4 && tpr > 384 && chunks <= 2 * 1024) continue;
+    const int rpb = tpr == 32 ? kRingTeams : 1;
+    const int per_sm =
+        (int)std::min<size_t>(kSmemSm / (2 * stage * rpb + kSmemBlock), std::max(1, kRingThreads / (tpr * rpb)));
+    if (per_sm < 1 || 2 * stage * rpb > kRingMax) break;
+    if (per_sm * tpr * rpb > most) {
+      most = per_sm * tpr * rpb;
+      const size_t room = std::min<size_t>(kSmemSm / per_sm - kSmemBlock, kRingMax);
+      pl = RingPlan{vpt, tpr, rpb, (int)std::min<size_t>(kRingStages, room / (stage * rpb)), per_sm};
+    }
+    if (most >= 512) break;
+  }
+  return most > 0;
 }
 
 template <class T, int OP, int VPT, int MAXT, RowLayout LAY>
@@ -848,7 +858,8 @@ cudaError_t launch_op(const RowQuantArgs& a, cudaStream_t st) {
     const int vpt = a.M <= 2 * sms ? 1 : 4;
     return vec ? launch_direct<T, OP, true>(a, vpt, st) : launch_direct<T, OP, false>(a, vpt, st);
   }
-  if (pl.vpt == 1) return launch_ring<T, OP, 1, 384>(a, pl, vec, stage, sms, dev, st);
+  if (pl.vpt == 1 && pl.tpr <= 384) return launch_ring<T, OP, 1, 384>(a, pl, vec, stage, sms, dev, st);
+  if (pl.vpt == 1) return launch_ring<T, OP, 1, 1024>(a, pl, vec, stage, sms, dev, st);
   if (pl.vpt == 2 && pl.tpr <= 384) return launch_ring<T, OP, 2, 384>(a, pl, vec, stage, sms, dev, st);
   if (pl.vpt == 2) return launch_ring<T, OP, 2, 1024>(a, pl, vec, stage, sms, dev, st);
   if (pl.tpr <= 384) return launch_ring<T, OP, 4, 384>(a, pl, vec, stage, sms, dev, st);
