@@ -112,6 +112,20 @@ def test_product(M, N, K, group, dtype):
     assert (buf[M] == 5).all() and (buf[:, N:] == 5).all()
 
 
+FEW_SHAPES = [                                               # on both sides of the few-token forms' limits
+    (1, 7200, 100, 0), (5, 14500, 333, 128), (8, 21500, 2000, 0), (7, 200, 8192, 0), (7, 200, 8193, 0), (2, 22600, 2048, 0),
+    (9, 4736, 65, 0), (9, 4737, 65, 0), (13, 4700, 1000, 64), (16, 300, 8192, 0), (16, 300, 8208, 0), (12, 17, 30, 0),
+    (17, 4736, 50, 0), (25, 4737, 500, 0), (31, 1000, 2047, 0), (32, 1000, 2049, 0), (32, 15, 2048, 128), (20, 9, 1, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K,group", FEW_SHAPES)
+def test_few_tokens(M, N, K, group, dtype):
+    test_product(M, N, K, group, dtype)
+
+
 @gpu
 @pytest.mark.parametrize("M", [2, 30, 80, 300])
 def test_longest_sums_of_the_lowest_code(M):

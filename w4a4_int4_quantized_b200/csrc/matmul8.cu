@@ -7,8 +7,8 @@
 // Few tokens are bound by reading the weights once, many by the tensor cores,
 // so there are three kernels:
 //
-// few_tokens_kernel   up to 8 tokens and small weights: a block owns 16 output
-//   channels, its warps split K.  Weights go from global memory straight into
+// few_tokens_kernel   up to 32 tokens and small weights: a block takes tiles of 16
+//   output channels, its warps split K.  Weights go from global memory straight into
 //   the registers of mma.sync m16n8k32: a lane loads 16 consecutive codes of a
 //   channel and of a token and uses them as the fragments of two products; both
 //   operands see the same permutation of k, which the sum does not notice.  The
@@ -136,76 +136,95 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// At most 8 tokens.  Bound by the latency of the loads: each warp has U k steps in
-// flight, and the block's weights are asked into L2 before the wait for the
-// previous kernel (a hint; the loads after the wait read memory as it then is).
-// Three blocks per SM leave room for the next kernel's blocks, whose hints then
-// run under this one.  One token, N = K = 4096, replayed back to back: 6.1 us
-// without the hint, 5.2 with it and U = 8 (two blocks per SM), 5.3 with U = 4; N =
-// 6144 9.6 and 6.0, N = 4096 with K = 1024 3.3 and 2.8.
-template <class O>
-__global__ void __launch_bounds__(kFewWarps * 32, 3) few_tokens_kernel(Matmul8Args p) {
-  constexpr int U = 4;             // k steps (64 codes) in flight per warp
-  __shared__ int part[kFewWarps][8][kFewRows + 1];
+// At most 8 NB tokens.  Bound by the latency of the loads: each warp has U k steps
+// in flight, and a tile's weights are asked into L2 a tile ahead, the first one's
+// before the wait for the previous kernel (a hint; the loads after the wait read
+// memory as it then is).  Resident blocks take the tiles in turn: one token, K =
+// 4096, replayed back to back, N = 4096 4.8 us (a block per tile 5.3, without the
+// hint 6.1), N = 10240 9.3 (a block per tile 12.6).  Three blocks per SM (two from 9
+// tokens on, whose fragments need the registers) leave room for the next kernel's
+// blocks, whose hints then run under this one.
+template <int NB, class O>
+__global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_kernel(Matmul8Args p) {
+  constexpr int U = NB <= 2 ? 4 : 2;   // k steps (64 codes) in flight per warp
+  __shared__ int part[2][kFewWarps][8 * NB][kFewRows + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int64_t n0 = (int64_t)blockIdx.x * kFewRows;
-  {
-    const int64_t n = n0 + (threadIdx.x & (kFewRows - 1));
+  const int64_t tiles = ((int64_t)p.N + kFewRows - 1) / kFewRows;
+  auto hint = [&](int64_t tile) {
+    const int64_t n = tile * kFewRows + (threadIdx.x & (kFewRows - 1));
     if (n < p.N)
       for (int k = (threadIdx.x / kFewRows) * 128; k < p.K; k += kFewWarps * 32 / kFewRows * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.B + n * p.ldb + k));
-  }
+  };
+  hint(blockIdx.x);
   grid_dependency_wait();
   grid_launch_dependents();
-  const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N, inx = g < p.M;
-  const int8_t* w0 = p.B + (n0 + g) * p.ldb;
-  const int8_t* w1 = p.B + (n0 + g + 8) * p.ldb;
-  const int8_t* x = p.A + (int64_t)g * p.lda;
-  int acc[4] = {};
   const int steps = p.K / 64;      // whole ones
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
-    uint4 a[U][2], b[U];
+  int buf = 0;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    if (tile + gridDim.x < tiles) hint(tile + gridDim.x);
+    const int64_t n0 = tile * kFewRows;
+    const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
+    const int8_t* w0 = p.B + (n0 + g) * p.ldb;
+    const int8_t* w1 = p.B + (n0 + g + 8) * p.ldb;
+    int acc[NB][4] = {};
+    for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
+      uint4 a[U][2], b[U][NB];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool go = s0 + u * kFewWarps < steps;
-      const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
-      a[u][0] = go && in0 ? ldg_stream(w0 + k0) : zero;
-      a[u][1] = go && in1 ? ldg_stream(w1 + k0) : zero;
+      for (int u = 0; u < U; ++u) {
+        const bool go = s0 + u * kFewWarps < steps;
+        const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
+        a[u][0] = go && in0 ? ldg_stream(w0 + k0) : zero;
+        a[u][1] = go && in1 ? ldg_stream(w1 + k0) : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          b[u][i] = s0 + u * kFewWarps < steps && 8 * i + g < p.M
+                        ? *reinterpret_cast<const uint4*>(p.A + (int64_t)(8 * i + g) * p.lda + k0)
+                        : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          mma_s8(acc[i], a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u][i].x, b[u][i].y);
+          mma_s8(acc[i], a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u][i].z, b[u][i].w);
+        }
+    }
+    if (p.K % 64 != 0 && warp == steps % kFewWarps) {
+      const int k0 = steps * 64 + 16 * t;
+      const uint4 a0 = load_last_codes(w0, k0, p.K, in0), a1 = load_last_codes(w1, k0, p.K, in1);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const uint4 b = load_last_codes(p.A + (int64_t)(8 * i + g) * p.lda, k0, p.K, 8 * i + g < p.M);
+        mma_s8(acc[i], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+        mma_s8(acc[i], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+      }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
-      b[u] = s0 + u * kFewWarps < steps && inx ? *reinterpret_cast<const uint4*>(x + k0) : zero;
+    for (int i = 0; i < NB; ++i) {
+      part[buf][warp][8 * i + 2 * t][g] = acc[i][0];
+      part[buf][warp][8 * i + 2 * t + 1][g] = acc[i][1];
+      part[buf][warp][8 * i + 2 * t][g + 8] = acc[i][2];
+      part[buf][warp][8 * i + 2 * t + 1][g + 8] = acc[i][3];
     }
+    __syncthreads();
+    // the buffer is written again two tiles on, behind the next tile's barrier
+    const int c = threadIdx.x % kFewRows;
+    const int64_t n = n0 + c;
+    for (int m = threadIdx.x / kFewRows; m < min(p.M, 8 * NB) && n < p.N; m += kFewWarps * 32 / kFewRows) {
+      int sum = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      mma_s8(acc, a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u].x, b[u].y);
-      mma_s8(acc, a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u].z, b[u].w);
+      for (int w = 0; w < kFewWarps; ++w) sum += part[buf][w][m][c];
+      const auto* bias = static_cast<const typename O::elem*>(p.bias);
+      const float y = dequant(sum, p.a_scale[m], p.b_scale[n], p.inv_group, bias ? O::to(bias[n]) : 0.0f, bias != nullptr);
+      static_cast<typename O::elem*>(p.Y)[(int64_t)m * p.ldy + n] = O::from(y);
     }
-  }
-  if (p.K % 64 != 0 && warp == steps % kFewWarps) {
-    const int k0 = steps * 64 + 16 * t;
-    const uint4 a0 = load_last_codes(w0, k0, p.K, in0), a1 = load_last_codes(w1, k0, p.K, in1);
-    const uint4 b = load_last_codes(x, k0, p.K, inx);
-    mma_s8(acc, a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-    mma_s8(acc, a0.z, a1.z, a0.w, a1.w, b.z, b.w);
-  }
-  part[warp][2 * t][g] = acc[0];
-  part[warp][2 * t + 1][g] = acc[1];
-  part[warp][2 * t][g + 8] = acc[2];
-  part[warp][2 * t + 1][g + 8] = acc[3];
-  __syncthreads();
-  const int m = threadIdx.x / kFewRows, c = threadIdx.x % kFewRows;
-  const int64_t n = n0 + c;
-  if (m < p.M && m < 8 && n < p.N) {
-    int sum = 0;
-#pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) sum += part[w][m][c];
-    const auto* bias = static_cast<const typename O::elem*>(p.bias);
-    const float y = dequant(sum, p.a_scale[m], p.b_scale[n], p.inv_group, bias ? O::to(bias[n]) : 0.0f, bias != nullptr);
-    static_cast<typename O::elem*>(p.Y)[(int64_t)m * p.ldy + n] = O::from(y);
   }
 }
 
@@ -862,10 +881,11 @@ cudaError_t launch_stream(const Matmul8Args& a, int split, int dev, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kern, a, split, tiles_m, tX, tW, err);
 }
 
-template <class O>
-cudaError_t launch_few(const Matmul8Args& a, cudaStream_t st) {
+template <int NB, class O>
+cudaError_t launch_few(const Matmul8Args& a, int sms, cudaStream_t st) {
+  const int64_t tiles = ((int64_t)a.N + kFewRows - 1) / kFewRows;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.N + kFewRows - 1) / kFewRows), 1, 1);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, (int64_t)sms * (NB == 1 ? 3 : 2)), 1, 1);
   cfg.blockDim = dim3(kFewWarps * 32, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -873,7 +893,7 @@ cudaError_t launch_few(const Matmul8Args& a, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<O>, a);
+  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<NB, O>, a);
 }
 
 // How many clusters of `size` CTAs of a kernel fit on the device at once (0
@@ -1005,14 +1025,21 @@ void consider_tiled(const Matmul8Args& a, int sms, int dev, Form& best) {
 // 27.5); 1000, 14336 x 4096 pair tiles 51 (65).
 template <class O>
 cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
-  // Up to 8 tokens, 24 MB of weights and 8192 codes of k: 25 MB 5.6 us against 9.6
-  // streamed, 34 MB 10.4 against 9.7; N = 1024 with K = 4096 3.0 against 4.6, with K
-  // = 16384 12.0 against 8.8.
-  if (a.M <= 8 && a.K <= 8192 && (int64_t)a.N * a.K <= (int64_t)24 << 20) return launch_few<O>(a, st);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
+  // Few tokens.  Up to 8, with 44 MB of weights and 8192 codes of k at most (us
+  // against the best streamed form, 8 tokens): 4096 x 4096 5.1 (6.6), 10240 x 4096 10.2
+  // (12.0), 14336 x 4096 14.1 (13.4), 4096 x 8192 9.6 (9.9), 4096 x 14336 14.6 (13.1, one
+  // token).  Up to 16, with every tile resident at once: 4096 x 4096 5.7 (6.7), 1024 x
+  // 1024 2.2 (4.0), 6144 x 4096 10.0 (8.8), 1024 x 16384 11.3 (9.0).  Up to 32, with
+  // 2048 codes besides: 1024 x 1024 2.6 (4.3), 4096 x 2048 5.1 (5.3), 1024 x 4096 5.6
+  // (5.1).
+  const bool resident = a.N <= 2 * sms * kFewRows;
+  if (a.M <= 8 && a.K <= 8192 && (int64_t)a.N * a.K <= (int64_t)44 << 20) return launch_few<1, O>(a, sms, st);
+  if (a.M <= 16 && a.K <= 8192 && resident) return launch_few<2, O>(a, sms, st);
+  if (a.M <= 32 && a.K <= 2048 && resident) return launch_few<4, O>(a, sms, st);
   Form f{0, 0, 0, 1e30f};
   if (a.M <= 16) consider_streamed<16, O>(a, sms, dev, f);
   else if (a.M <= 32) consider_streamed<32, O>(a, sms, dev, f);
