@@ -80,20 +80,56 @@ __device__ __forceinline__ float dequant(int acc, float sx, float sw, float inv_
   return has_bias ? __fadd_rn(y, bias) : y;
 }
 
-// Four consecutive elements, n of them inside the row; vec: the address is
-// aligned to their size.
+// Four consecutive elements at an address aligned to their size, n of them
+// inside the row.
 template <class O>
-__device__ __forceinline__ void store4(typename O::elem* p, int n, bool vec, const float (&y)[4]) {
+__device__ __forceinline__ void store4(typename O::elem* p, int n, const float (&y)[4]) {
   typename O::elem e[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) e[j] = O::from(y[j]);
-  if (vec && n >= 4) {
+  if (n >= 4) {
     if constexpr (sizeof(typename O::elem) == 2) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(e);
     else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(e);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j < n) p[j] = e[j];
+  }
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+// A row of 128 sums finished by a warp.  A lane's columns are four neighbours
+// where they can be stored at once (vec), else every 32nd, so that a store covers
+// whole sectors all the same.
+__device__ __forceinline__ int lane_col(bool vec, int lane, int j) { return vec ? 4 * lane + j : lane + 32 * j; }
+
+// This lane's four sums of the row at `row`, in this CTA or a peer.
+__device__ __forceinline__ uint4 ld_row4(uint32_t row, int lane, bool vec, bool remote) {
+  if (vec) return remote ? ld_cluster_v4(row + 16 * lane) : ld_shared_v4(row + 16 * lane);
+  const uint32_t at = row + 4 * lane;
+  if (remote) return make_uint4(ld_cluster_u32(at), ld_cluster_u32(at + 128), ld_cluster_u32(at + 256), ld_cluster_u32(at + 384));
+  return make_uint4(ld_shared_u32(at), ld_shared_u32(at + 128), ld_shared_u32(at + 256), ld_shared_u32(at + 384));
+}
+
+// The row's elements from y on, n of them inside the matrix.
+template <class O>
+__device__ __forceinline__ void store_row4(typename O::elem* y, int64_t n, int lane, bool vec, const float (&v)[4]) {
+  if (vec) {
+    if (4 * lane < n) store4<O>(y + 4 * lane, (int)min((int64_t)4, n - 4 * lane), v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane + 32 * j < n) y[lane + 32 * j] = O::from(v[j]);
   }
 }
 
@@ -111,20 +147,19 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// The codes that a row's last step (64 codes) has at k0: up to 16, zeros past K,
-// nothing read there.  Out of line: one warp of a block calls it, and only where
-// K is not a multiple of 64.
-__device__ __noinline__ uint4 load_last_codes(const int8_t* row, int k0, int K, bool in) {
-  if (!in || k0 >= K) return make_uint4(0u, 0u, 0u, 0u);
-  if (k0 + 16 <= K) return ldg_stream(row + k0);
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  for (int i = 0; i < K - k0; ++i) {
-    const uint32_t b = (uint32_t)(uint8_t)row[k0 + i] << (8 * (i & 3));
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j == i >> 2) w[j] |= b;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+// The last n < 16 codes of a row, at p (16-byte aligned), zeros behind them; nothing
+// past the row is read.  Four loads of falling size that do not wait for one
+// another: one token, N = 175, K = 668 2.1 us, with a load per code 6.9.
+__device__ __forceinline__ uint4 load_last_codes(const int8_t* p, int n) {
+  uint2 lo = make_uint2(0u, 0u);
+  uint64_t b4 = 0, b2 = 0, b1 = 0;
+  if (n & 8) lo = *reinterpret_cast<const uint2*>(p);
+  if (n & 4) b4 = *reinterpret_cast<const uint32_t*>(p + (n & 8));
+  if (n & 2) b2 = *reinterpret_cast<const uint16_t*>(p + (n & 12));
+  if (n & 1) b1 = *reinterpret_cast<const uint8_t*>(p + (n & 14));
+  const uint64_t t = b4 | b2 << (8 * (n & 4)) | b1 << (8 * (n & 6));
+  const uint32_t t0 = (uint32_t)t, t1 = (uint32_t)(t >> 32);
+  return n & 8 ? make_uint4(lo.x, lo.y, t0, t1) : make_uint4(t0, t1, 0u, 0u);
 }
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -160,7 +195,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
   hint(blockIdx.x);
   grid_dependency_wait();
   grid_launch_dependents();
-  const int steps = p.K / 64;      // whole ones
+  const int steps = (p.K + 63) / 64;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   int buf = 0;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
@@ -174,8 +209,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
       uint4 a[U][2], b[U][NB];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool go = s0 + u * kFewWarps < steps;
         const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
+        const bool go = k0 + 16 <= p.K;
         a[u][0] = go && in0 ? ldg_stream(w0 + k0) : zero;
         a[u][1] = go && in1 ? ldg_stream(w1 + k0) : zero;
       }
@@ -184,7 +219,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
         const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
 #pragma unroll
         for (int i = 0; i < NB; ++i)
-          b[u][i] = s0 + u * kFewWarps < steps && 8 * i + g < p.M
+          b[u][i] = k0 + 16 <= p.K && 8 * i + g < p.M
                         ? *reinterpret_cast<const uint4*>(p.A + (int64_t)(8 * i + g) * p.lda + k0)
                         : zero;
       }
@@ -196,14 +231,18 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
           mma_s8(acc[i], a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u][i].z, b[u][i].w);
         }
     }
-    if (p.K % 64 != 0 && warp == steps % kFewWarps) {
-      const int k0 = steps * 64 + 16 * t;
-      const uint4 a0 = load_last_codes(w0, k0, p.K, in0), a1 = load_last_codes(w1, k0, p.K, in1);
+    if (const int last = p.K % 16; last != 0 && warp == steps % kFewWarps) {   // the lanes that own its 16 codes
+      const int k0 = p.K - last;
+      const bool own = t == k0 / 16 % 4;
+      const uint4 a0 = load_last_codes(w0 + k0, own && in0 ? last : 0), a1 = load_last_codes(w1 + k0, own && in1 ? last : 0);
+      uint4 b[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        b[i] = load_last_codes(p.A + (int64_t)(8 * i + g) * p.lda + k0, own && 8 * i + g < p.M ? last : 0);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        const uint4 b = load_last_codes(p.A + (int64_t)(8 * i + g) * p.lda, k0, p.K, 8 * i + g < p.M);
-        mma_s8(acc[i], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-        mma_s8(acc[i], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+        mma_s8(acc[i], a0.x, a1.x, a0.y, a1.y, b[i].x, b[i].y);
+        mma_s8(acc[i], a0.z, a1.z, a0.w, a1.w, b[i].z, b[i].w);
       }
     }
 #pragma unroll
@@ -366,12 +405,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int tm, tn;
     tile_at(t0, pl, tm, tn);
     sm0 = (int64_t)tm * 2 * BM + (int64_t)half * BM;
-    sn0 = (int64_t)tn * BN + lane * 4;
+    sn0 = (int64_t)tn * BN;
 #pragma unroll
     for (int c = 0; c < kG; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t n = sn0 + c * 128 + j;
+        const int64_t n = sn0 + c * 128 + lane_col(p.vec_out, lane, j);
         const auto* bias = static_cast<const typename O::elem*>(p.bias);
         ssw[c][j] = n < p.N ? p.b_scale[n] : 0.0f;
         sbs[c][j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
@@ -499,7 +538,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
     } else {
       const uint32_t stg = base + (uint32_t)(C::kRing + ew * kStageBytes);
-      const int cl = (lane & 7) * 4, rl = lane >> 3;  // this lane's columns and first row when rows are read back
+      // A lane's columns and first row of four when rows are read back: four
+      // columns where they can be stored at once, else a column of four rows, so
+      // that a store covers whole sectors all the same.
+      const bool vec = p.vec_out;
+      const int cl = vec ? (lane & 7) * 4 : lane, rl = vec ? lane >> 3 : 0;
       int i = 0;
       for (int64_t t = t0; t < tiles; t += tstep, ++i) {
         const int b = i & 1;
@@ -515,8 +558,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int j = 0; j < 4; ++j) {
             const int64_t n = n0 + ch * 32 + j;
             const auto* bias = static_cast<const typename O::elem*>(p.bias);
-            sw[ch][j] = n < p.N ? p.b_scale[n] : 0.0f;
-            bs[ch][j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
+            const bool in = n < p.N && (vec || j == 0);
+            sw[ch][j] = in ? p.b_scale[n] : 0.0f;
+            bs[ch][j] = bias && in ? O::to(bias[n]) : 0.0f;
           }
         if (!mbar_wait_cluster(&bar->acc_full[b], (uint32_t)(i / 2) & 1u)) {
           set_device_error(err, kDevErrTimeoutAcc);
@@ -541,23 +585,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                          : "memory");
           __syncwarp();
           const int64_t n = n0 + ch * 32;
+          const bool hb = p.bias != nullptr;
+          if (vec) {
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const int row = r * 4 + rl;
-            uint4 a;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w)
-                         : "r"(stg + (uint32_t)(row * kStagePitch + cl * 4)));
-            const float s = __shfl_sync(0xFFFFFFFFu, sx, row);
-            const int64_t m = m0 + row;
-            if (m < p.M && n < p.N) {
-              const bool hb = p.bias != nullptr;
-              const float y[4] = {dequant((int)a.x, s, sw[ch][0], p.inv_group, bs[ch][0], hb),
-                                  dequant((int)a.y, s, sw[ch][1], p.inv_group, bs[ch][1], hb),
-                                  dequant((int)a.z, s, sw[ch][2], p.inv_group, bs[ch][2], hb),
-                                  dequant((int)a.w, s, sw[ch][3], p.inv_group, bs[ch][3], hb)};
-              store4<O>(static_cast<typename O::elem*>(p.Y) + m * p.ldy + n, (int)min((int64_t)4, p.N - n),
-                        p.vec_out, y);
+            for (int r = 0; r < 8; ++r) {
+              const int row = r * 4 + rl;
+              const uint4 a = ld_shared_v4(stg + (uint32_t)(row * kStagePitch + cl * 4));
+              const float s = __shfl_sync(0xFFFFFFFFu, sx, row);
+              const int64_t m = m0 + row;
+              if (m < p.M && n < p.N) {
+                const float y[4] = {dequant((int)a.x, s, sw[ch][0], p.inv_group, bs[ch][0], hb),
+                                    dequant((int)a.y, s, sw[ch][1], p.inv_group, bs[ch][1], hb),
+                                    dequant((int)a.z, s, sw[ch][2], p.inv_group, bs[ch][2], hb),
+                                    dequant((int)a.w, s, sw[ch][3], p.inv_group, bs[ch][3], hb)};
+                store4<O>(static_cast<typename O::elem*>(p.Y) + m * p.ldy + n, (int)min((int64_t)4, p.N - n), y);
+              }
+            }
+          } else {
+            typename O::elem* y = static_cast<typename O::elem*>(p.Y) + m0 * p.ldy + n;
+#pragma unroll 8
+            for (int row = 0; row < 32; ++row, y += p.ldy) {
+              const int a = (int)ld_shared_u32(stg + (uint32_t)(row * kStagePitch + cl * 4));
+              const float s = __shfl_sync(0xFFFFFFFFu, sx, row);
+              if (m0 + row < p.M && n < p.N) *y = O::from(dequant(a, s, sw[ch][0], p.inv_group, bs[ch][0], hb));
             }
           }
         }
@@ -591,7 +641,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < kG; ++c)
             if (q < S && (h == 0 || two))
-              v[h][q][c] = ld_cluster_v4(peer[q] + (uint32_t)((r + h * step) * C::kPartPitch + (c * 128 + lane * 4) * 4));
+              v[h][q][c] = ld_row4(peer[q] + (uint32_t)((r + h * step) * C::kPartPitch + c * 512), lane, p.vec_out, true);
 #pragma unroll
       for (int h = 0; h < kRows; ++h) {
         if (h == 1 && !two) break;
@@ -607,13 +657,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               a[3] += (int)v[h][q][c].w;
             }
           const int64_t n = n0 + c * 128;
-          if (n >= p.N) continue;
           const bool hb = p.bias != nullptr;
           float y[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], sx[h], ssw[c][j], p.inv_group, sbs[c][j], hb);
-          store4<O>(static_cast<typename O::elem*>(p.Y) + (m0 + r + h * step) * p.ldy + n, (int)min((int64_t)4, p.N - n),
-                    p.vec_out, y);
+          store_row4<O>(static_cast<typename O::elem*>(p.Y) + (m0 + r + h * step) * p.ldy + n, p.N - n, lane, p.vec_out, y);
         }
       }
     }
@@ -656,12 +704,6 @@ struct StreamBars {
   uint64_t full[8], empty[8], acc_full;
   uint32_t tmem_base;
 };
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
 
 // One tile of 128 output channels, or (split > 1, a cluster of that many CTAs)
 // one slice of its K.  Warp 0 loads, warp 1 issues the products, warps 4 to 7
@@ -765,13 +807,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   }
 
   // What the final step needs from global memory, while the products run.
-  const int64_t n = (int64_t)tile * kStreamRows + 4 * lane;
+  const int64_t n0 = (int64_t)tile * kStreamRows;
   const auto* bias = static_cast<const typename O::elem*>(p.bias);
   float sw[4], bs[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    sw[j] = n + j < p.N ? p.b_scale[n + j] : 0.0f;
-    bs[j] = bias && n + j < p.N ? O::to(bias[n + j]) : 0.0f;
+    const int64_t n = n0 + lane_col(p.vec_out, lane, j);
+    sw[j] = n < p.N ? p.b_scale[n] : 0.0f;
+    bs[j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
   }
   if (threadIdx.x >= 64 && threadIdx.x < 64 + NT) {    // warps 2 to 5
     const int m = (int)threadIdx.x - 64;
@@ -806,10 +849,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll
   for (int r = 0; r < 8; ++r) peer[r] = split > 1 && r < split ? map_to_rank(base, (uint32_t)r) : base;
   for (int m = q + warp * split; m < tokens; m += (kStreamThreads / 32) * split) {
-    const uint32_t at = (uint32_t)(m * C::kPartPitch + 16 * lane);
+    const uint32_t at = (uint32_t)(m * C::kPartPitch);
     int a[4];
     if (split == 1) {
-      const uint4 v = ld_shared_v4(base + at);
+      const uint4 v = ld_row4(base + at, lane, p.vec_out, false);
       a[0] = (int)v.x;
       a[1] = (int)v.y;
       a[2] = (int)v.z;
@@ -818,7 +861,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       uint4 v[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r < split) v[r] = ld_cluster_v4(peer[r] + at);
+        if (r < split) v[r] = ld_row4(peer[r] + at, lane, p.vec_out, true);
       a[0] = a[1] = a[2] = a[3] = 0;
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -829,14 +872,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           a[3] += (int)v[r].w;
         }
     }
-    if (n < p.N) {
-      const float s = sx[m];
-      float y[4];
+    const float s = sx[m];
+    float y[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], s, sw[j], p.inv_group, bs[j], bias != nullptr);
-      store4<O>(static_cast<typename O::elem*>(p.Y) + (int64_t)(m0 + m) * p.ldy + n, (int)min((int64_t)4, p.N - n),
-                p.vec_out, y);
-    }
+    for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], s, sw[j], p.inv_group, bs[j], bias != nullptr);
+    store_row4<O>(static_cast<typename O::elem*>(p.Y) + (int64_t)(m0 + m) * p.ldy + n0, p.N - n0, lane, p.vec_out, y);
   }
   if (split > 1) cluster_sync();                       // the sums stay readable until every CTA has taken them
   if (warp == 2) {
