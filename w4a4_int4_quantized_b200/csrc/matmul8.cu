@@ -47,6 +47,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -63,11 +64,19 @@ struct OutBf16 {
   using elem = __nv_bfloat16;
   static __device__ __forceinline__ elem from(float f) { return __float2bfloat16_rn(f); }
   static __device__ __forceinline__ float to(elem e) { return __bfloat162float(e); }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 };
 struct OutFp16 {
   using elem = __half;
   static __device__ __forceinline__ elem from(float f) { return __float2half_rn(f); }
   static __device__ __forceinline__ float to(elem e) { return __half2float(e); }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
 };
 struct OutFp32 {
   using elem = float;
@@ -101,6 +110,22 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
+}
+__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
@@ -274,8 +299,8 @@ constexpr int kTileThreads = 384;
 constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;
 constexpr int kIssueBar = 1;             // named barrier: MMA warp + the warp that waits for it
-constexpr int kStagePitch = 32 * 4 + 16;                    // epilogue staging: row of 32 int32, bank-spread
-constexpr int kStageBytes = 32 * kStagePitch;               // per epilogue warp
+constexpr int kStagePitch = 128 + 16;                       // epilogue staging: 128 bytes of a row, bank-spread
+constexpr int kStageBytes = 32 * kStagePitch + 1024;        // per epilogue warp: 32 rows; its columns' scales and bias
 constexpr int kSmemLimit = 232448;
 
 template <int BN>
@@ -298,6 +323,55 @@ struct TileCfg {
   static_assert(BM * kPartPitch <= kRing + kEpi, "partials fit where the ring was");
   static_assert(kSmem <= kSmemLimit, "shared memory budget");
 };
+
+// 32 rows of 128 bytes that a warp has staged, stored to y and ldy elements on;
+// `rows` and `cols` of them are inside the matrix, rows of y are aligned to gran
+// bytes.  16: four rows per store; else a row per store of 4 bytes per lane, or
+// half of one of 2.
+template <class E>
+__device__ __forceinline__ void store_rows(uint32_t stg, E* y, int64_t ldy, int64_t rows, int64_t cols, int gran, int lane) {
+  constexpr int kV = 16 / (int)sizeof(E), kW = 4 / (int)sizeof(E);
+  using bits = typename std::conditional<sizeof(E) == 2, uint16_t, uint32_t>::type;
+  bits* out = reinterpret_cast<bits*>(y);
+  if (gran == 16) {
+    const int c = (lane & 7) * kV;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int row = r * 4 + (lane >> 3);
+      const uint4 a = ld_shared_v4(stg + (uint32_t)(row * kStagePitch + (lane & 7) * 16));
+      if (row < rows && c < cols) {
+        bits* to = out + row * ldy + c;
+        if (c + kV <= cols) {
+          *reinterpret_cast<uint4*>(to) = a;
+        } else {
+          const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int j = 0; j < kV - 1; ++j)
+            if (c + j < cols) to[j] = (bits)(w[j / kW] >> (16 * (j % kW)));
+        }
+      }
+    }
+  } else if (gran == 4) {
+    const int c = lane * kW;
+#pragma unroll 8
+    for (int row = 0; row < 32; ++row) {
+      const uint32_t a = ld_shared_u32(stg + (uint32_t)(row * kStagePitch + lane * 4));
+      if (row < rows && c < cols) {
+        bits* to = out + row * ldy + c;
+        if (c + kW <= cols) *reinterpret_cast<uint32_t*>(to) = a;
+        else *to = (bits)a;
+      }
+    }
+  } else if constexpr (sizeof(E) == 2) {
+#pragma unroll 8
+    for (int row = 0; row < 32; ++row)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint16_t a = ld_shared_u16(stg + (uint32_t)(row * kStagePitch + h * 64 + lane * 2));
+        if (row < rows && h * 32 + lane < cols) out[row * ldy + h * 32 + lane] = a;
+      }
+  }
+}
 
 struct TileBars {
   uint64_t full[12], empty[12], acc_full[2], acc_empty[2];
@@ -519,7 +593,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int quad = warp & 3, hc = ew >> 2;
     constexpr int kCols = BN / 2;                    // columns of a warp
     if constexpr (SPLIT) {
-      if (mbar_wait_cluster(&bar->acc_full[0], 0u)) {
+      if (__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&bar->acc_full[0], 0u))) {
         tc_fence_after();
         const uint32_t row = base + (uint32_t)((quad * 32 + lane) * C::kPartPitch + hc * kCols * 4);
 #pragma unroll
@@ -537,78 +611,88 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         set_device_error(err, kDevErrTimeoutAcc);
       }
     } else {
-      const uint32_t stg = base + (uint32_t)(C::kRing + ew * kStageBytes);
-      // A lane's columns and first row of four when rows are read back: four
-      // columns where they can be stored at once, else a column of four rows, so
-      // that a store covers whole sectors all the same.
-      const bool vec = p.vec_out;
-      const int cl = vec ? (lane & 7) * 4 : lane, rl = vec ? lane >> 3 : 0;
+      // A lane owns a row: 32 sums from tensor memory (the next 32 under way),
+      // scaled and packed, staged 128 bytes a row, then stored by rows.  The scales
+      // and bias of the next tile are fetched a tile ahead.
+      constexpr int kJ = kCols / 32;
+      constexpr int kGroup = 4 / (int)sizeof(typename O::elem);        // chunks of 32 columns in 128 bytes
+      const uint32_t stg = base + (uint32_t)(C::kRing + ew * kStageBytes), sc = stg + 32 * kStagePitch;
+      const auto* bias = static_cast<const typename O::elem*>(p.bias);
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p.Y) | (uintptr_t)(p.ldy * (int64_t)sizeof(typename O::elem));
+      const int gran = at % 16 == 0 ? 16 : at % 4 == 0 ? 4 : 2;
+      float nsw[kJ], nbs[kJ], nsx;
+      auto fetch = [&](int64_t t) {
+        int tm, tn;
+        tile_at(t, pl, tm, tn);
+        const int64_t m = (int64_t)tm * 2 * BM + (int64_t)half * BM + quad * 32 + lane;
+        nsx = m < p.M ? p.a_scale[m] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          const int64_t n = (int64_t)tn * BN + hc * kCols + j * 32 + lane;
+          nsw[j] = n < p.N ? p.b_scale[n] : 0.0f;
+          nbs[j] = bias && n < p.N ? O::to(bias[n]) : -0.0f;           // y + -0 is y
+        }
+      };
+      if (t0 < tiles) fetch(t0);
       int i = 0;
       for (int64_t t = t0; t < tiles; t += tstep, ++i) {
         const int b = i & 1;
         int tm, tn;
         tile_at(t, pl, tm, tn);
         const int64_t m0 = (int64_t)tm * 2 * BM + (int64_t)half * BM + quad * 32;
-        const int64_t n0 = (int64_t)tn * BN + hc * kCols + cl;
-        const float sx = m0 + lane < p.M ? p.a_scale[m0 + lane] : 0.0f;
-        float sw[kCols / 32][4], bs[kCols / 32][4];
+        const int64_t n0 = (int64_t)tn * BN + hc * kCols;
+        const float sx = nsx;
+        __syncwarp();                                   // the last tile's scales are read
 #pragma unroll
-        for (int ch = 0; ch < kCols / 32; ++ch)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + ch * 32 + j;
-            const auto* bias = static_cast<const typename O::elem*>(p.bias);
-            const bool in = n < p.N && (vec || j == 0);
-            sw[ch][j] = in ? p.b_scale[n] : 0.0f;
-            bs[ch][j] = bias && in ? O::to(bias[n]) : 0.0f;
-          }
-        if (!mbar_wait_cluster(&bar->acc_full[b], (uint32_t)(i / 2) & 1u)) {
+        for (int j = 0; j < kJ; ++j) {
+          st_shared_f32(sc + (uint32_t)(j * 128 + lane * 4), nsw[j]);
+          st_shared_f32(sc + (uint32_t)(512 + j * 128 + lane * 4), nbs[j]);
+        }
+        if (t + tstep < tiles) fetch(t + tstep);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&bar->acc_full[b], (uint32_t)(i / 2) & 1u))) {
           set_device_error(err, kDevErrTimeoutAcc);
           break;
         }
         tc_fence_after();
+        const uint32_t ta = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BN + hc * kCols);
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(ta, v[0]);
 #pragma unroll
-        for (int ch = 0; ch < kCols / 32; ++ch) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BN + hc * kCols + ch * 32), v);
-          tmem_wait_ld();
-          if (ch == kCols / 32 - 1) {                 // the accumulator may be overwritten
+        for (int ch = 0; ch < kJ; ++ch) {
+          tmem_wait_ld_x32(v[ch & 1]);
+          if (ch < kJ - 1) {
+            tmem_ld_32x32b_x32(ta + (uint32_t)(32 * (ch + 1)), v[(ch + 1) & 1]);
+          } else {                                      // the accumulator may be overwritten
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote(&bar->acc_empty[b], lead);
           }
-          __syncwarp();                               // the last chunk's rows are read
+          if (ch % kGroup == 0) __syncwarp();           // the last rows are read
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stg + (uint32_t)(lane * kStagePitch + j * 16)),
-                         "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3])
-                         : "memory");
-          __syncwarp();
-          const int64_t n = n0 + ch * 32;
-          const bool hb = p.bias != nullptr;
-          if (vec) {
+          for (int j = 0; j < 4; ++j) {                 // eight columns at a time
+            float y[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const int row = r * 4 + rl;
-              const uint4 a = ld_shared_v4(stg + (uint32_t)(row * kStagePitch + cl * 4));
-              const float s = __shfl_sync(0xFFFFFFFFu, sx, row);
-              const int64_t m = m0 + row;
-              if (m < p.M && n < p.N) {
-                const float y[4] = {dequant((int)a.x, s, sw[ch][0], p.inv_group, bs[ch][0], hb),
-                                    dequant((int)a.y, s, sw[ch][1], p.inv_group, bs[ch][1], hb),
-                                    dequant((int)a.z, s, sw[ch][2], p.inv_group, bs[ch][2], hb),
-                                    dequant((int)a.w, s, sw[ch][3], p.inv_group, bs[ch][3], hb)};
-                store4<O>(static_cast<typename O::elem*>(p.Y) + m * p.ldy + n, (int)min((int64_t)4, p.N - n), y);
-              }
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t col = sc + (uint32_t)(ch * 128 + j * 32 + h * 16);
+              const float4 w = ld_shared_f4(col), bb = ld_shared_f4(col + 512);
+              const uint32_t* a = &v[ch & 1][8 * j + 4 * h];
+              y[4 * h] = dequant((int)a[0], sx, w.x, p.inv_group, bb.x, true);
+              y[4 * h + 1] = dequant((int)a[1], sx, w.y, p.inv_group, bb.y, true);
+              y[4 * h + 2] = dequant((int)a[2], sx, w.z, p.inv_group, bb.z, true);
+              y[4 * h + 3] = dequant((int)a[3], sx, w.w, p.inv_group, bb.w, true);
             }
-          } else {
-            typename O::elem* y = static_cast<typename O::elem*>(p.Y) + m0 * p.ldy + n;
-#pragma unroll 8
-            for (int row = 0; row < 32; ++row, y += p.ldy) {
-              const int a = (int)ld_shared_u32(stg + (uint32_t)(row * kStagePitch + cl * 4));
-              const float s = __shfl_sync(0xFFFFFFFFu, sx, row);
-              if (m0 + row < p.M && n < p.N) *y = O::from(dequant(a, s, sw[ch][0], p.inv_group, bs[ch][0], hb));
+            const uint32_t to = stg + (uint32_t)(lane * kStagePitch + (ch % kGroup * 32 + 8 * j) * (int)sizeof(typename O::elem));
+            if constexpr (sizeof(typename O::elem) == 2) {
+              st_shared_v4(to, O::pack(y[0], y[1]), O::pack(y[2], y[3]), O::pack(y[4], y[5]), O::pack(y[6], y[7]));
+            } else {
+              st_shared_v4(to, __float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+              st_shared_v4(to + 16, __float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7]));
             }
+          }
+          if (ch % kGroup == kGroup - 1) {
+            __syncwarp();
+            const int64_t n = n0 + (ch - kGroup + 1) * 32;
+            store_rows<typename O::elem>(stg, static_cast<typename O::elem*>(p.Y) + m0 * p.ldy + n, p.ldy, p.M - m0, p.N - n, gran, lane);
           }
         }
       }
@@ -821,7 +905,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     sx[m] = m < tokens ? p.a_scale[m0 + m] : 0.0f;
   }
   if (warp >= 4) {
-    if (mbar_wait(&bar->acc_full, 0u)) {
+    if (__all_sync(0xFFFFFFFFu, mbar_wait(&bar->acc_full, 0u))) {
       tc_fence_after();
       constexpr int CH = NT < 32 ? NT : 32;
       const int c = (warp - 4) * 32 + lane;            // this thread's channel of the tile
