@@ -25,17 +25,18 @@
 // tile_kernel         a cluster of two CTAs owns a 256 x BN tile and issues
 //   tcgen05.mma kind::i8 in its pair form: each CTA holds 128 rows of A and
 //   BN / 2 of B per stage, 128 bytes of k wide in the 128-byte swizzle that
-//   TMA writes.  8192 x 24576 x 8192: 1048 us alone, 3150 TOPS, the tensor pipe 78%
-//   active; 4608 x 4096 x 4096: 56 us.  Two accumulators of BN columns in tensor memory let the
-//   epilogue of one tile run under the products of the next.  TMA fills what
-//   lies past M, N or K with zeros.
+//   TMA writes.  Two accumulators of BN columns in tensor memory let the epilogue
+//   of one tile run under the products of the next.  8192 x 24576 x 8192: 1023 to 1055
+//   us alone, 3130 to 3230 TOPS; 4608 x 4096 x 4096: 53 us; 8192 x 4096 x 256, bound by
+//   its epilogues (3.1 us a tile; staged as int32 and scaled on the way out they took
+//   5.2): 25 us.  TMA fills what lies past M, N or K with zeros.
 //     warp 0       TMA loads (both CTAs; both complete on the even CTA's
 //                  barrier)
 //     warp 1       MMA issue (even CTA)
 //     warp 3       polls the barriers that the MMA warp depends on
-//     warps 4-11   epilogue: tensor memory -> registers -> shared memory
-//                  (int32, 32 x 32 per warp) -> row-major registers, scales,
-//                  coalesced stores
+//     warps 4-11   epilogue: tensor memory -> registers, a row per lane ->
+//                  scaled and packed -> shared memory (32 rows of 128 bytes per
+//                  warp) -> coalesced stores
 //   SPLIT: too few tiles for the GPU; a cluster of 2 S CTAs owns one tile, pair
 //   q takes a slice of K, and the int32 partials are summed exactly through
 //   distributed shared memory, rows interleaved over the pairs.
@@ -1100,53 +1101,64 @@ struct Form {
   float cost;
 };
 
-// The streaming kernel.  A k-block costs 0.25 (16 or 32 tokens), 0.26 (64) or
-// 0.37 (128), 1.4 times that where SMs hold two CTAs, and no less than the
-// weights' way from memory; a launch 2.4 to 4 with its first loads and last
-// step; a split 0.8 for its cluster barriers and its sums' way between SMs at 3.5
-// MB per us.
+// What every form moves at least, in us.
+template <class O>
+float memory_time(const Matmul8Args& a) {
+  return ((float)a.N * (float)a.K + (float)a.M * (float)a.K + (float)a.M * (float)a.N * sizeof(typename O::elem)) * (1.0f / 6.5e6f);
+}
+
+// The streaming kernel.  A k-block costs 0.26 (16 to 64 tokens; with 64 1.15 times
+// that where rows of 128 codes lie in two lines of memory) or 0.37 (128), 1.4 times
+// that where SMs hold two CTAs; a launch 2.8 to 4 with its first loads and last step,
+// a further wave 3 to 5.5 besides its k-blocks of 0.36 or 0.42; a split 0.8 for its
+// cluster barriers and its sums' way between SMs at 3.5 MB per us.
 template <int NT, class O>
 void consider_streamed(const Matmul8Args& a, int sms, int dev, Form& best) {
-  constexpr float kb = NT <= 32 ? 0.25f : NT == 64 ? 0.26f : 0.37f, base = NT <= 32 ? 2.4f : NT == 64 ? 3.0f : 4.0f;
+  constexpr float base = NT <= 32 ? 2.8f : NT == 64 ? 3.0f : 4.0f, wave = NT <= 32 ? 3.0f : NT == 64 ? 4.0f : 5.5f;
+  const float lines = NT == 64 && (a.lda | a.ldb) % BK != 0 ? 1.15f : 1.0f;
+  const float kb = lines * (NT <= 64 ? 0.26f : 0.37f), wave_kb = lines * (NT <= 64 ? 0.36f : 0.42f);
   const int64_t tiles = ((int64_t)a.N + kStreamRows - 1) / kStreamRows * (((int64_t)a.M + NT - 1) / NT);
   const int nk = (a.K + BK - 1) / BK;
   if (tiles > 0x7FFFFFFF / 8) return;
-  const float memory = (float)a.N * (float)a.K * (1.0f / 6.5e6f);
   for (int s = 1; s <= 8; s *= 2) {
     if (s > 1 && (nk < 2 * s || tiles * s > 2 * (int64_t)sms || tiles > resident_streams<NT, O>(s, dev))) break;
-    const int64_t ctas = tiles * s;
-    const float waves = (float)((ctas + 2 * sms - 1) / (2 * sms));
-    float cost = std::max(memory, waves * (float)((nk + s - 1) / s) * kb * (ctas > sms ? 1.4f : 1.0f)) + base;
+    const int64_t ctas = tiles * s, waves = (ctas + 2 * sms - 1) / (2 * sms);
+    const float per = (float)((nk + s - 1) / s);
+    const float work = per * kb * (ctas > sms ? 1.4f : 1.0f) + (float)(waves - 1) * (wave + per * wave_kb);
+    float cost = std::max(memory_time<O>(a), work) + base;
     if (s > 1) cost += 0.8f + (float)(ctas * NT * kStreamRows * 4 / s * (s - 1)) * (1.0f / 3.5e6f);
     if (cost < best.cost) best = Form{NT, 0, s, cost};
   }
 }
 
-// The pair kernel.  A k-block costs 0.29 (256 x 128) or 0.30 (256 x 256), a launch
-// 4.9 or 6.5, a split 1.75; whole tiles walk in rounds of SMs / 2.  Clusters that are
-// not all resident at once would cost a second round (256 x 4096 x 12288 in
-// quarters 34 us, in thirds 19.4), so they are not considered.
+// The pair kernel.  A k-block costs 0.28 (256 x 128) or 0.30 (256 x 256), a launch
+// 4.7 or 5.8, a split 1.75; whole tiles walk in rounds of SMs / 2, none of which is shorter
+// than its epilogue: 1.75 or 3.1.  Clusters that are not all resident at once would
+// cost a second round (256 x 4096 x 12288 in quarters 34 us, in thirds 19.4), so they
+// are not considered.
 template <int BN, class O>
 void consider_tiled(const Matmul8Args& a, int sms, int dev, Form& best) {
-  constexpr float kb = BN == 256 ? 0.30f : 0.29f, base = BN == 256 ? 6.5f : 4.9f;
+  constexpr float kb = BN == 256 ? 0.30f : 0.28f, base = BN == 256 ? 5.8f : 4.7f, epilogue = BN == 256 ? 3.1f : 1.75f;
   const int64_t tiles = (((int64_t)a.M + 2 * BM - 1) / (2 * BM)) * (((int64_t)a.N + BN - 1) / BN);
   const int nk = (a.K + BK - 1) / BK, pairs = sms / 2;
-  const float memory = (float)a.N * (float)a.K * (1.0f / 6.5e6f);
   for (int s = 1; s <= 4; ++s) {
     if (s > 1 && (nk < 2 * s || tiles * s > pairs)) break;
     if (s > 1 && tiles > resident_tiles<BN, O>(s, dev)) continue;
-    const float rounds = s > 1 ? 1.0f : (float)((tiles + pairs - 1) / pairs);
-    const float cost = std::max(memory, rounds * (float)((nk + s - 1) / s) * kb) + base + (s > 1 ? 1.75f : 0.0f);
+    const int64_t rounds = s > 1 ? 1 : (tiles + pairs - 1) / pairs;
+    const float per = (float)((nk + s - 1) / s) * kb;
+    const float work = per + (float)(rounds - 1) * std::max(per, epilogue);
+    const float cost = std::max(memory_time<O>(a), work) + base + (s > 1 ? 1.75f : 0.0f);
     if (cost < best.cost) best = Form{0, BN, s, cost};
   }
 }
 
-// The form with the least modelled time.  Over 72 sizes (12 to 2000 tokens, N 200 to
-// 14336, K 500 to 12288) it is 2% above the best form measured on average, 14% at
-// most; us measured: 16 tokens, 28672 x 4096 streamed 22.1 (pair tiles 33); 64, 4096
-// x 4096 streamed in quarters 8.0 (11); 256, 1024 x 1024 streamed 5.1 (7.0); 333, 1013
-// x 2995 streamed 7.7 (9.3); 333, 4096 x 12288 pair tiles in halves 22.5 (streamed
-// 27.5); 1000, 14336 x 4096 pair tiles 51 (65).
+// The form with the least modelled time.  Over 186 sizes (9 to 8192 tokens, N 8 to
+// 28672, K 16 to 16384) it is 2.3% above the best form measured on average, 21% at
+// most but for one product of 10 channels; us measured: 16 tokens, 28672 x 4096
+// streamed 22.1 (pair tiles 33); 64, 4096 x 4096 streamed in quarters 8.0 (11); 256,
+// 1024 x 1024 streamed 5.1 (7.0); 333, 1013 x 2995 streamed 7.7 (9.3); 333, 4096 x
+// 12288 pair tiles in halves 22.5 (streamed 27.5); 1000, 14336 x 4096 pair tiles 51
+// (65); 7404, 18199 x 27 pair tiles 114 (180).
 template <class O>
 cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
   int dev = 0, sms = 0;
