@@ -90,37 +90,85 @@ __device__ __forceinline__ void load8(const typename T::word* p, int n, float2 (
   }
 }
 
-template <class T, bool VEC>
+// Eight elements to a 16-byte aligned address where n > 0.
+template <class T>
 __device__ __forceinline__ void store8(typename T::word* p, int n, const float2 (&f)[4]) {
-  if constexpr (VEC) {
-    if (n <= 0) return;
-    uint32_t u[T::kWords];
+  if (n <= 0) return;
+  uint32_t u[T::kWords];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (T::kWords == 4) {
-        u[j] = T::pack(f[j]);
-      } else {
-        u[2 * j] = __float_as_uint(f[j].x);
-        u[2 * j + 1] = __float_as_uint(f[j].y);
-      }
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (T::kWords == 4) {
+      u[j] = T::pack(f[j]);
+    } else {
+      u[2 * j] = __float_as_uint(f[j].x);
+      u[2 * j + 1] = __float_as_uint(f[j].y);
     }
+  }
 #pragma unroll
-    for (int i = 0; i < T::kWords / 4; ++i)
-      reinterpret_cast<uint4*>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
-  } else {
+  for (int i = 0; i < T::kWords / 4; ++i)
+    reinterpret_cast<uint4*>(p)[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+}
+
+// The words of a window moved down by `bytes` (0 to 15, the same in the whole warp).
+template <int IN, int OUT>
+__device__ __forceinline__ void shift_words(const uint32_t (&w)[IN], uint32_t bytes, uint32_t (&out)[OUT]) {
+  static_assert(IN >= OUT + 4, "a window of one 16-byte granule more");
+  const uint32_t bits = (bytes & 3u) * 8u;
+  switch (bytes >> 2) {
+    case 0:
+#pragma unroll
+      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], bits);
+      break;
+    case 1:
+#pragma unroll
+      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 1], w[i + 2], bits);
+      break;
+    case 2:
+#pragma unroll
+      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 2], w[i + 3], bits);
+      break;
+    default:
+#pragma unroll
+      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 3], i + 4 < IN ? w[i + 4] : 0u, bits);
+  }
+}
+
+// Eight consecutive elements at any element alignment, n of them inside the row,
+// by the 16-byte granules that hold them, which bring up to 14 bytes of the row's
+// neighbours along.  EDGE: rows near the operand's ends (lo, hi), where a granule
+// that passes them is not read and the chunk goes element by element.
+template <class T, bool EDGE>
+__device__ __forceinline__ void load8_window(const typename T::word* p, int n, const void* lo, const void* hi,
+                                             float2 (&f)[4]) {
+  constexpr int NW = T::kWords;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const uint32_t off = (uint32_t)(at & 15u);
+  const int bytes = n > 0 ? (int)off + min(n, 8) * (int)sizeof(typename T::word) : 0;
+  if (EDGE && n > 0 &&
+      (at - off < reinterpret_cast<uintptr_t>(lo) || at - off + ((bytes + 15) & ~15) > reinterpret_cast<uintptr_t>(hi))) {
+    load8<T, false>(p, n, f);
+    return;
+  }
+  uint32_t w[NW + 4], u[NW];
+#pragma unroll
+  for (int i = 0; i < NW / 4 + 1; ++i) {
+    const uint4 g = 16 * i < bytes ? reinterpret_cast<const uint4*>(at - off)[i] : make_uint4(0u, 0u, 0u, 0u);
+    w[4 * i] = g.x;
+    w[4 * i + 1] = g.y;
+    w[4 * i + 2] = g.z;
+    w[4 * i + 3] = g.w;
+  }
+  shift_words(w, off, u);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (NW == 4) f[j] = T::two(u[j]);
+    else f[j] = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+  }
+  if (n < 8) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uint32_t lo, hi;
-      if constexpr (T::kWords == 4) {
-        const uint32_t w = T::pack(f[j]);
-        lo = w & 0xFFFFu;
-        hi = w >> 16;
-      } else {
-        lo = __float_as_uint(f[j].x);
-        hi = __float_as_uint(f[j].y);
-      }
-      if (2 * j < n) p[2 * j] = (typename T::word)lo;
-      if (2 * j + 1 < n) p[2 * j + 1] = (typename T::word)hi;
+      if (2 * j >= n) f[j].x = 0.0f;
+      if (2 * j + 1 >= n) f[j].y = 0.0f;
     }
   }
 }
@@ -281,7 +329,7 @@ struct RowShared {
   float sum[32], max[2][32];
 };
 
-template <class T, int VPT, bool VEC, bool FULL>
+template <class T, int VPT, bool FULL>
 __device__ __forceinline__ void store_sum(const float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t,
                                           int tpr) {
   if (!p.H) return;
@@ -289,7 +337,31 @@ __device__ __forceinline__ void store_sum(const float2 (&f)[VPT][4], const RowQu
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int e = (v * tpr + t) * 8;
-    store8<T, VEC>(h + e, left<FULL>(p.K, e), f[v]);
+    store8<T>(h + e, left<FULL>(p.K, e), f[v]);
+  }
+}
+template <class T, int VPT>
+__device__ __forceinline__ void store_sum_elements(const float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t,
+                                                   int tpr) {
+  if (!p.H) return;
+  auto* h = static_cast<typename T::word*>(p.H) + row * p.ldh;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = (v * tpr + t) * 8, n = p.K - e;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t lo, hi;
+      if constexpr (T::kWords == 4) {
+        const uint32_t w = T::pack(f[v][j]);
+        lo = w & 0xFFFFu;
+        hi = w >> 16;
+      } else {
+        lo = __float_as_uint(f[v][j].x);
+        hi = __float_as_uint(f[v][j].y);
+      }
+      if (2 * j < n) h[e + 2 * j] = (typename T::word)lo;
+      if (2 * j + 1 < n) h[e + 2 * j + 1] = (typename T::word)hi;
+    }
   }
 }
 template <int VPT>
@@ -339,10 +411,15 @@ __device__ __forceinline__ void quantize_row(float2 (&f)[VPT][4], const RowQuant
   }
 }
 
+__device__ __forceinline__ void times8(float2 (&f)[4], const float2 (&g)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(f[j], g[j]);
+}
+
 // The norm of a row h in f, its rotation, scale and codes: a reduction for the
 // sum of squares and one for max |y|, and two more with h scaled by a power of two
-// where the squares pass fp32's range.  gamma(v, g) gives the weights of chunk
-// v; taken() runs in every thread once all have their inputs in registers.
+// where the squares pass fp32's range.  gamma(f) multiplies by the
+// weights; taken() runs in every thread once all have their inputs in registers.
 template <int VPT, bool VEC, bool FULL, class Gamma, class Taken>
 __device__ __forceinline__ void norm_row(float2 (&f)[VPT][4], const RowQuantArgs& p, int64_t row, int t, int tpr,
                                          RowShared& sh, Gamma&& gamma, Taken&& taken) {
@@ -359,15 +436,7 @@ __device__ __forceinline__ void norm_row(float2 (&f)[VPT][4], const RowQuantArgs
     eps = eps * k * k;
   }
   scale_row(f, inv_sqrt(fmaf(ss, p.inv_k, eps)));
-  if (p.gamma) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      float2 g[4];
-      gamma(v, g);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[v][j] = __fmul2_rn(f[v][j], g[j]);
-    }
-  }
+  if (p.gamma) gamma(f);
   rotate_row(f, p.group);
   const float m = row_max(thread_max(f), sh.max[0], nwarps);
   quantize_row<VPT, VEC, FULL>(f, p, row, t, tpr, m);
@@ -384,144 +453,32 @@ __device__ __forceinline__ void plain_row(float2 (&f)[VPT][4], const RowQuantArg
   quantize_row<VPT, VEC, FULL>(f, p, row, t, tpr, m);
 }
 
+// The weights of a thread's chunks, all loads before the first use.  VEC: aligned
+// and whole; else whole chunks of aligned weights at once, so that no load waits
+// behind a branch, and the rest element by element.
+template <class T, int VPT, bool VEC>
+__device__ __forceinline__ void load_gamma(const RowQuantArgs& p, int t, int tpr, float2 (&g)[VPT][4]) {
+  const auto* w = static_cast<const typename T::word*>(p.gamma);
+  const int whole = VEC || (reinterpret_cast<uintptr_t>(w) & 15u) == 0 ? p.K & ~7 : 0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int e = (v * tpr + t) * 8;
+    load8<T, true>(w + e, whole - e, g[v]);
+  }
+  if (!VEC && whole < p.K) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int e = (v * tpr + t) * 8;
+      if (e >= whole && e < p.K) load8<T, false>(w + e, p.K - e, g[v]);
+    }
+  }
+}
+
 // The second operand into f: added (OP 0) or gated by it (OP 1).
 template <int OP>
 __device__ __forceinline__ void combine8(float2 (&f)[4], const float2 (&g)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) f[j] = OP == 0 ? __fadd2_rn(f[j], g[j]) : silu_mul2(f[j], g[j]);
-}
-
-// OP 0: norm (A = x, B = residual or null, gamma, H or null); OP 1: silu (A =
-// gate, B = up).  VPT: chunks of 8 per thread.  Rows straight from global
-// memory: few or short rows, at any alignment (VEC: all on 16 bytes), and rows
-// whose inputs do not fit in shared memory.  One row per team of tpr threads,
-// bound by the latency of its loads and two reductions: 1 x 4096 bf16 2.4 us.
-template <class T, int OP, int VPT, int MAXT, bool VEC>
-__global__ void __launch_bounds__(MAXT) row_quantize_kernel(RowQuantArgs p, int tpr) {
-  using W = typename T::word;
-  __shared__ RowShared sh;
-  const int rpb = blockDim.x / tpr;            // > 1 only where a row is one warp
-  const int t = threadIdx.x % tpr;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
-  if (row >= p.M) return;
-  const W* a = static_cast<const W*>(p.A) + row * p.lda;
-  const W* b = p.B ? static_cast<const W*>(p.B) + row * p.ldb : nullptr;
-  float2 f[VPT][4];
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    const int e = (v * tpr + t) * 8;
-    load8<T, VEC>(a + e, p.K - e, f[v]);
-  }
-  if (b) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int e = (v * tpr + t) * 8;
-      float2 g[4];
-      load8<T, VEC>(b + e, p.K - e, g);
-      combine8<OP>(f[v], g);
-    }
-  }
-  if constexpr (OP == 1) {
-    plain_row<VPT, VEC, false>(f, p, row, t, tpr, sh.max[0], [] {});
-  } else {
-    store_sum<T, VPT, VEC, false>(f, p, row, t, tpr);
-    norm_row<VPT, VEC, false>(
-        f, p, row, t, tpr, sh,
-        [&](int v, float2 (&g)[4]) {
-          const int e = (v * tpr + t) * 8;
-          load8<T, VEC>(static_cast<const W*>(p.gamma) + e, p.K - e, g);
-        },
-        [] {});
-  }
-}
-
-// Bytes of a contiguous row into shared memory, completing on a barrier (16-byte
-// aligned addresses and sizes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-// 8 elements from shared memory (16-byte aligned), zeros where n <= 0.
-template <class T>
-__device__ __forceinline__ void smem8(uint32_t addr, int n, float2 (&f)[4]) {
-  uint32_t u[T::kWords];
-#pragma unroll
-  for (int i = 0; i < T::kWords / 4; ++i) {
-    u[4 * i] = u[4 * i + 1] = u[4 * i + 2] = u[4 * i + 3] = 0u;
-    if (n > 0)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(u[4 * i]), "=r"(u[4 * i + 1]), "=r"(u[4 * i + 2]), "=r"(u[4 * i + 3])
-                   : "r"(addr + 16 * i));
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if constexpr (T::kWords == 4) f[j] = T::two(u[j]);
-    else f[j] = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-  }
-}
-
-// How the rows of a ring lie: every thread has whole chunks (kWhole), the last
-// threads may have none (kAligned), or rows start off the 16-byte alignment or
-// end inside a chunk (kShifted).
-enum RowLayout { kWhole, kAligned, kShifted };
-
-// Words i0 .. i0 + n - 1 of a window, moved down by `bytes` (0 to 15, the same in
-// the whole block).
-template <int IN, int OUT>
-__device__ __forceinline__ void shift_words(const uint32_t (&w)[IN], uint32_t bytes, uint32_t (&out)[OUT]) {
-  static_assert(IN >= OUT + 4, "a window of one 16-byte granule more");
-  const uint32_t bits = (bytes & 3u) * 8u;
-  switch (bytes >> 2) {
-    case 0:
-#pragma unroll
-      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], bits);
-      break;
-    case 1:
-#pragma unroll
-      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 1], w[i + 2], bits);
-      break;
-    case 2:
-#pragma unroll
-      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 2], w[i + 3], bits);
-      break;
-    default:
-#pragma unroll
-      for (int i = 0; i < OUT; ++i) out[i] = __funnelshift_r(w[i + 3], i + 4 < IN ? w[i + 4] : 0u, bits);
-  }
-}
-
-// The first n of 8 elements whose row begins `off` bytes into a 16-byte granule
-// of shared memory; the rest are zero.  at: the granule that the first one lies
-// in once `off` is added (the same `off` for every chunk of a row).
-template <class T>
-__device__ __forceinline__ void smem8_shifted(uint32_t at, uint32_t off, int n, float2 (&f)[4]) {
-  constexpr int NW = T::kWords;
-  uint32_t w[NW + 4], u[NW];
-#pragma unroll
-  for (int i = 0; i < NW / 4 + 1; ++i) {
-    w[4 * i] = w[4 * i + 1] = w[4 * i + 2] = w[4 * i + 3] = 0u;
-    if (n > 0)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
-                   : "r"(at + 16 * i));
-  }
-  shift_words(w, off, u);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if constexpr (NW == 4) f[j] = T::two(u[j]);
-    else f[j] = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-  }
-  if (n < 8) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (2 * j >= n) f[j].x = 0.0f;
-      if (2 * j + 1 >= n) f[j].y = 0.0f;
-    }
-  }
 }
 
 // A row of the sum to global memory at any element alignment.  A whole chunk's
@@ -588,6 +545,137 @@ __device__ __forceinline__ void store_sum_shifted(const float2 (&f)[VPT][4], con
           if constexpr (NW == 4) h[e + i] = (W)((i & 1) ? u[i / 2] >> 16 : u[i / 2] & 0xFFFFu);
           else h[e + i] = u[i];
         }
+    }
+  }
+}
+
+// How the direct kernel reads and writes rows: at 16-byte alignment, by the
+// granules around their chunks, or, rows of one warp, element by element (a SiLU of
+// 8027 x 37 fp32 4.0 us, by granules 4.9; a norm of 16384 x 100 bf16 10.1 and 12.6;
+// but 488 x 4993 18.2 and 10.5).
+enum RowLoads { kAligned16, kWindows, kElements };
+
+// OP 0: norm (A = x, B = residual or null, gamma, H or null); OP 1: silu (A =
+// gate, B = up).  VPT: chunks of 8 per thread.  Rows straight from global
+// memory: few or short rows, at any alignment (VEC: all on 16 bytes), and rows
+// whose inputs do not fit in shared memory.  One row per team of tpr threads,
+// bound by the latency of its loads and two reductions: 1 x 4096 bf16 2.4 us.
+template <class T, int OP, int VPT, int MAXT, RowLoads LOADS>
+__global__ void __launch_bounds__(MAXT) row_quantize_kernel(RowQuantArgs p, int tpr) {
+  using W = typename T::word;
+  __shared__ RowShared sh;
+  const int rpb = blockDim.x / tpr;            // > 1 only where a row is one warp
+  const int t = threadIdx.x % tpr;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+  if (row >= p.M) return;
+  const W* a = static_cast<const W*>(p.A) + row * p.lda;
+  const W* b = p.B ? static_cast<const W*>(p.B) + row * p.ldb : nullptr;
+  float2 f[VPT][4];
+  auto load = [&](auto read) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int e = (v * tpr + t) * 8;
+      read(a + e, p.K - e, p.A, p.lda, f[v]);
+    }
+    if (b) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int e = (v * tpr + t) * 8;
+        float2 g[4];
+        read(b + e, p.K - e, p.B, p.ldb, g);
+        combine8<OP>(f[v], g);
+      }
+    }
+  };
+  if constexpr (LOADS == kAligned16) {
+    load([](const W* x, int n, const void*, int64_t, float2 (&y)[4]) { load8<T, true>(x, n, y); });
+  } else if constexpr (LOADS == kElements) {
+    load([](const W* x, int n, const void*, int64_t, float2 (&y)[4]) { load8<T, false>(x, n, y); });
+  } else if (row > 0 && row < p.M - 1) {
+    load([](const W* x, int n, const void*, int64_t, float2 (&y)[4]) { load8_window<T, false>(x, n, nullptr, nullptr, y); });
+  } else {
+    load([&](const W* x, int n, const void* lo, int64_t ld, float2 (&y)[4]) {
+      load8_window<T, true>(x, n, lo, static_cast<const W*>(lo) + (int64_t)(p.M - 1) * ld + p.K, y);
+    });
+  }
+  if constexpr (OP == 1) {
+    plain_row<VPT, LOADS == kAligned16, false>(f, p, row, t, tpr, sh.max[0], [] {});
+  } else {
+    if constexpr (LOADS == kAligned16) store_sum<T, VPT, false>(f, p, row, t, tpr);
+    else if constexpr (LOADS == kWindows) store_sum_shifted<T, VPT>(f, p, row, t, tpr);
+    else store_sum_elements<T, VPT>(f, p, row, t, tpr);
+    norm_row<VPT, LOADS == kAligned16, false>(
+        f, p, row, t, tpr, sh,
+        [&](float2 (&y)[VPT][4]) {
+          float2 g[VPT][4];
+          load_gamma<T, VPT, LOADS == kAligned16>(p, t, tpr, g);
+#pragma unroll
+          for (int v = 0; v < VPT; ++v) times8(y[v], g[v]);
+        },
+        [] {});
+  }
+}
+
+// Bytes of a contiguous row into shared memory, completing on a barrier (16-byte
+// aligned addresses and sizes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// 8 elements from shared memory (16-byte aligned), zeros where n <= 0.
+template <class T>
+__device__ __forceinline__ void smem8(uint32_t addr, int n, float2 (&f)[4]) {
+  uint32_t u[T::kWords];
+#pragma unroll
+  for (int i = 0; i < T::kWords / 4; ++i) {
+    u[4 * i] = u[4 * i + 1] = u[4 * i + 2] = u[4 * i + 3] = 0u;
+    if (n > 0)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u[4 * i]), "=r"(u[4 * i + 1]), "=r"(u[4 * i + 2]), "=r"(u[4 * i + 3])
+                   : "r"(addr + 16 * i));
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (T::kWords == 4) f[j] = T::two(u[j]);
+    else f[j] = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+  }
+}
+
+// How the rows of a ring lie: every thread has whole chunks (kWhole), the last
+// threads may have none (kAligned), or rows start off the 16-byte alignment or
+// end inside a chunk (kShifted).
+enum RowLayout { kWhole, kAligned, kShifted };
+
+// The first n of 8 elements whose row begins `off` bytes into a 16-byte granule
+// of shared memory; the rest are zero.  at: the granule that the first one lies
+// in once `off` is added (the same `off` for every chunk of a row).
+template <class T>
+__device__ __forceinline__ void smem8_shifted(uint32_t at, uint32_t off, int n, float2 (&f)[4]) {
+  constexpr int NW = T::kWords;
+  uint32_t w[NW + 4], u[NW];
+#pragma unroll
+  for (int i = 0; i < NW / 4 + 1; ++i) {
+    w[4 * i] = w[4 * i + 1] = w[4 * i + 2] = w[4 * i + 3] = 0u;
+    if (n > 0)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(at + 16 * i));
+  }
+  shift_words(w, off, u);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (NW == 4) f[j] = T::two(u[j]);
+    else f[j] = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+  }
+  if (n < 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (2 * j >= n) f[j].x = 0.0f;
+      if (2 * j + 1 >= n) f[j].y = 0.0f;
     }
   }
 }
@@ -718,21 +806,26 @@ __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAX
       plain_row<VPT, LAY != kShifted, FULL>(f, p, row, t, tpr, sh.max[parity], taken);
     } else {
       if constexpr (LAY == kShifted) store_sum_shifted<T, VPT>(f, p, row, t, tpr);
-      else store_sum<T, VPT, true, FULL>(f, p, row, t, tpr);
+      else store_sum<T, VPT, FULL>(f, p, row, t, tpr);
       norm_row<VPT, LAY != kShifted, FULL>(
           f, p, row, t, tpr, sh,
-          [&](int v, float2 (&g)[4]) {
-            if constexpr (kHoldGamma) {
-              g[0] = T::two(gw[v].x);
-              g[1] = T::two(gw[v].y);
-              g[2] = T::two(gw[v].z);
-              g[3] = T::two(gw[v].w);
-            } else {
-              const int e = (v * tpr + t) * 8;
-              const W* w = static_cast<const W*>(p.gamma) + e;
-              const int n = left<FULL>(p.K, e);
-              if (LAY != kShifted || (n >= 8 && (reinterpret_cast<uintptr_t>(p.gamma) & 15u) == 0)) load8<T, true>(w, n, g);
-              else load8<T, false>(w, n, g);
+          [&](float2 (&y)[VPT][4]) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+              float2 g[4];
+              if constexpr (kHoldGamma) {
+                g[0] = T::two(gw[v].x);
+                g[1] = T::two(gw[v].y);
+                g[2] = T::two(gw[v].z);
+                g[3] = T::two(gw[v].w);
+              } else {
+                const int e = (v * tpr + t) * 8;
+                const W* w = static_cast<const W*>(p.gamma) + e;
+                const int n = left<FULL>(p.K, e);
+                if (LAY != kShifted || (n >= 8 && (reinterpret_cast<uintptr_t>(p.gamma) & 15u) == 0)) load8<T, true>(w, n, g);
+                else load8<T, false>(w, n, g);
+              }
+              times8(y[v], g);
             }
           },
           taken);
@@ -762,18 +855,35 @@ cudaError_t launch_rows(Kernel kern, int64_t grid, int threads, size_t smem, cud
 
 int threads_per_row(int chunks, int vpt) { return ((chunks + vpt - 1) / vpt + 31) / 32 * 32; }
 
-template <class T, int OP, bool VEC>
-cudaError_t launch_direct(const RowQuantArgs& a, int vpt, cudaStream_t st) {
+// Rows of one warp, four to a block.
+template <class T, int OP, RowLoads LOADS>
+cudaError_t launch_warp_rows(const RowQuantArgs& a, int vpt, cudaStream_t st) {
+  const int64_t blocks = ((int64_t)a.M + 3) / 4;
+  if (vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 128, LOADS>, blocks, 128, 0, st, a, 32);
+  if (vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 128, LOADS>, blocks, 128, 0, st, a, 32);
+  return launch_rows(row_quantize_kernel<T, OP, 4, 128, LOADS>, blocks, 128, 0, st, a, 32);
+}
+template <class T, int OP, RowLoads LOADS>
+cudaError_t launch_block_rows(const RowQuantArgs& a, int vpt, int tpr, cudaStream_t st) {
+  if (vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 1024, LOADS>, a.M, tpr, 0, st, a, tpr);
+  if (vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 1024, LOADS>, a.M, tpr, 0, st, a, tpr);
+  return launch_rows(row_quantize_kernel<T, OP, 4, 1024, LOADS>, a.M, tpr, 0, st, a, tpr);
+}
+
+// Chunks per thread of the direct kernel: one, the shortest chain, where there are
+// at most two rows per SM or every row is resident at once, else two (norm of 600 x
+// 768 bf16 2.7 us with one, 2.9 with two; off the alignment 3.3 and 4.4; 600 x 4096
+// 7.5 and 5.6; 900 x 5120 gated 6.8 with two, 7.5 with four), four where one warp then
+// has a row (2000 x 768 4.5 us, with two 4.9) or 1024 threads cannot hold it in two.
+template <class T, int OP>
+cudaError_t launch_direct(const RowQuantArgs& a, bool vec, int sms, cudaStream_t st) {
   const int chunks = (a.K + 7) / 8;
+  int vpt = a.M <= 2 * sms || (int64_t)a.M * threads_per_row(chunks, 1) <= (int64_t)1024 * sms ? 1 : vec && chunks <= 128 ? 4 : 2;
   while (vpt < 4 && (chunks + vpt - 1) / vpt > 1024) vpt *= 2;
   while (vpt > 1 && chunks <= 32 * (vpt / 2)) vpt /= 2;
   const int tpr = threads_per_row(chunks, vpt);
-  const int rpb = tpr == 32 ? 4 : 1;
-  const int64_t blocks = ((int64_t)a.M + rpb - 1) / rpb;
-  if (vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 1024, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
-  if (vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 1024, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
-  if (tpr <= 512) return launch_rows(row_quantize_kernel<T, OP, 4, 512, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
-  return launch_rows(row_quantize_kernel<T, OP, 4, 1024, VEC>, blocks, tpr * rpb, 0, st, a, tpr);
+  if (tpr == 32) return vec ? launch_warp_rows<T, OP, kAligned16>(a, vpt, st) : launch_warp_rows<T, OP, kElements>(a, vpt, st);
+  return vec ? launch_block_rows<T, OP, kAligned16>(a, vpt, tpr, st) : launch_block_rows<T, OP, kWindows>(a, vpt, tpr, st);
 }
 
 // An SM's shared memory for rings: 228 KB less 2 KB for each block (the runtime's
@@ -854,10 +964,7 @@ cudaError_t launch_op(const RowQuantArgs& a, cudaStream_t st) {
   RingPlan pl;
   const size_t stage = (size_t)slot_bytes((uint32_t)(a.K * es), !vec) * (a.B ? 2 : 1);
   const bool much = stage >= 24u * 1024u || (size_t)a.M * stage >= (size_t)32 << 20;
-  if (a.M <= 2 * sms || !much || a.K * es < 16 || !plan_ring(a.K, stage, pl)) {
-    const int vpt = a.M <= 2 * sms ? 1 : 4;
-    return vec ? launch_direct<T, OP, true>(a, vpt, st) : launch_direct<T, OP, false>(a, vpt, st);
-  }
+  if (a.M <= 2 * sms || !much || a.K * es < 16 || !plan_ring(a.K, stage, pl)) return launch_direct<T, OP>(a, vec, sms, st);
   if (pl.vpt == 1 && pl.tpr <= 384) return launch_ring<T, OP, 1, 384>(a, pl, vec, stage, sms, dev, st);
   if (pl.vpt == 1) return launch_ring<T, OP, 1, 1024>(a, pl, vec, stage, sms, dev, st);
   if (pl.vpt == 2 && pl.tpr <= 384) return launch_ring<T, OP, 2, 384>(a, pl, vec, stage, sms, dev, st);
