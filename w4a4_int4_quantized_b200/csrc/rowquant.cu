@@ -956,14 +956,19 @@ cudaError_t launch_op(const RowQuantArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
-  // The ring pays where rows are long or many: norm of 1200 x 4096 bf16 11.2 us
-  // against 9.8 direct, 16384 x 100 15.9 against 10.0, but 4608 x 4096 27.2 against
-  // 31; SiLU of 600 x 14336 12.4 against 15.7.  At most two rows per SM go direct
-  // with a chunk per thread, the shortest chain.  Rows under 16 bytes have no
-  // granule of their own to copy.
+  // The ring pays where rows are long or many; us direct, ring.  Aligned: norm of 1200
+  // x 4096 bf16 9.4, 11.1, of 3000 x 4096 19.2, 20.1, of 4608 x 4096 31, 27, of 2000 x 8192
+  // 29.6, 26.0; SiLU of 2000 x 5120 12.7, 15.1, of 600 x 14336 15.7, 12.4.  Off the
+  // alignment, where the stored sum costs the ring more registers than it saves:
+  // norm of 1200 x 8195 28, 35, of 8192 x 4099 80, 95, of 13340 x 5222 168, 163, of 1623 x
+  // 14470 69, 55, without a residual of 16384 x 1030 fp32 36, 48, of 16384 x 5003 124, 101;
+  // SiLU, which stores none, of 1021 x 5461 fp32 18.0, 13.2, of 1500 x 6001
+  // 17.9, 16.5.  At most two rows per SM go direct; rows under 16 bytes have no granule
+  // of their own to copy.
   RingPlan pl;
-  const size_t stage = (size_t)slot_bytes((uint32_t)(a.K * es), !vec) * (a.B ? 2 : 1);
-  const bool much = stage >= 24u * 1024u || (size_t)a.M * stage >= (size_t)32 << 20;
+  const size_t slot = slot_bytes((uint32_t)(a.K * es), !vec), stage = slot * (a.B ? 2 : 1);
+  const bool much = !vec && OP == 0 ? slot >= 24u * 1024u || (size_t)a.M * slot >= (size_t)80 << 20
+                                    : stage >= 24u * 1024u || (size_t)a.M * stage >= (size_t)(vec ? 64 : 32) << 20;
   if (a.M <= 2 * sms || !much || a.K * es < 16 || !plan_ring(a.K, stage, pl)) return launch_direct<T, OP>(a, vec, sms, st);
   if (pl.vpt == 1 && pl.tpr <= 384) return launch_ring<T, OP, 1, 384>(a, pl, vec, stage, sms, dev, st);
   if (pl.vpt == 1) return launch_ring<T, OP, 1, 1024>(a, pl, vec, stage, sms, dev, st);
