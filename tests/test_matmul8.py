@@ -127,6 +127,14 @@ def test_few_tokens(M, N, K, group, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("N,K", [(5304, 109), (5294, 110), (5299, 109), (5295, 109), (5303, 1000), (5296, 1000)])
+def test_many_tiles_by_alignment(N, K, dtype):
+    """Several tiles per pair of SMs; rows of Y at 16, 4 and 2 bytes, and ends inside a store."""
+    test_product(2550, N, K, 64, dtype)
+
+
+@gpu
 @pytest.mark.parametrize("M", [2, 30, 80, 300])
 def test_longest_sums_of_the_lowest_code(M):
     import torch

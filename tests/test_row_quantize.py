@@ -253,6 +253,21 @@ def test_silu(M, K, group, pad, offset, dtype):
     check_codes(silu64(_f64(gate), _f64(up)), group, silu_c(_f64(gate)), _f64(q), _f64(s))
 
 
+FORMS = [                                            # M, K, group, pad, offset: the ways rows are read and worked on
+    (300, 1537, 0, 3, 1), (1500, 1537, 0, 1, 0), (300, 12289, 0, 0, 1), (310, 20003, 0, 5, 2), (2000, 300, 0, 3, 1),
+    (900, 40, 0, 1, 1), (5000, 1000, 0, 0, 0), (3000, 1152, 128, 8, 0), (3000, 1152, 128, 5, 0), (600, 640, 64, 3, 1),
+    (2, 9001, 0, 7, 3), (1, 2001, 0, 0, 5), (2, 5, 0, 0, 1), (400, 7, 0, 0, 1), (299, 4160, 64, 1, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K,group,pad,offset", FORMS)
+def test_forms(M, K, group, pad, offset, dtype):
+    test_norm(M, K, group, pad, offset, dtype)
+    test_silu(M, K, group, pad, offset, dtype)
+
+
 @gpu
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("K", [40, 1027, 4096])
@@ -365,6 +380,13 @@ def test_weights_of_extreme_size(M, group):
         q, s, _ = w4.w8a8_add_rmsnorm_quantize(X, gamma, EPS, group)
         torch.cuda.synchronize()
         check_codes(norm64(_f64(X), None, _f64(gamma), EPS)[1], group, 21, _f64(q), _f64(s))
+
+
+@gpu
+@pytest.mark.parametrize("M,K", [(300, 1537), (500, 5001), (300, 12289), (4, 30001)])
+def test_sum_in_place_off_the_alignment(M, K):
+    for _ in range(3):
+        test_sum_in_place_of_an_input(M, K)
 
 
 @gpu
