@@ -90,14 +90,14 @@ __device__ __forceinline__ float dequant(int acc, float sx, float sw, float inv_
   return has_bias ? __fadd_rn(y, bias) : y;
 }
 
-// Four consecutive elements at an address aligned to their size, n of them
-// inside the row.
+// Four consecutive elements, n of them inside the row; vec: the address is
+// aligned to their size.
 template <class O>
-__device__ __forceinline__ void store4(typename O::elem* p, int n, const float (&y)[4]) {
+__device__ __forceinline__ void store4(typename O::elem* p, int n, bool vec, const float (&y)[4]) {
   typename O::elem e[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) e[j] = O::from(y[j]);
-  if (n >= 4) {
+  if (vec && n >= 4) {
     if constexpr (sizeof(typename O::elem) == 2) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(e);
     else *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(e);
   } else {
@@ -134,31 +134,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
-// A row of 128 sums finished by a warp.  A lane's columns are four neighbours
-// where they can be stored at once (vec), else every 32nd, so that a store covers
-// whole sectors all the same.
-__device__ __forceinline__ int lane_col(bool vec, int lane, int j) { return vec ? 4 * lane + j : lane + 32 * j; }
-
-// This lane's four sums of the row at `row`, in this CTA or a peer.
-__device__ __forceinline__ uint4 ld_row4(uint32_t row, int lane, bool vec, bool remote) {
-  if (vec) return remote ? ld_cluster_v4(row + 16 * lane) : ld_shared_v4(row + 16 * lane);
-  const uint32_t at = row + 4 * lane;
-  if (remote) return make_uint4(ld_cluster_u32(at), ld_cluster_u32(at + 128), ld_cluster_u32(at + 256), ld_cluster_u32(at + 384));
-  return make_uint4(ld_shared_u32(at), ld_shared_u32(at + 128), ld_shared_u32(at + 256), ld_shared_u32(at + 384));
-}
-
-// The row's elements from y on, n of them inside the matrix.
-template <class O>
-__device__ __forceinline__ void store_row4(typename O::elem* y, int64_t n, int lane, bool vec, const float (&v)[4]) {
-  if (vec) {
-    if (4 * lane < n) store4<O>(y + 4 * lane, (int)min((int64_t)4, n - 4 * lane), v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lane + 32 * j < n) y[lane + 32 * j] = O::from(v[j]);
-  }
-}
-
 // ------------------------------------------------------------------ few tokens
 constexpr int kFewWarps = 8;
 constexpr int kFewRows = 16;     // output channels per block
@@ -173,19 +148,24 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// The last n < 16 codes of a row, at p (16-byte aligned), zeros behind them; nothing
-// past the row is read.  Four loads of falling size that do not wait for one
-// another: one token, N = 175, K = 668 2.1 us, with a load per code 6.9.
+// Up to 16 codes at p (16-byte aligned) of which the row still has n, zeros behind
+// them; nothing past the row is read.  Fewer come by four loads of falling size that
+// do not wait for one another: one token, N = 175, K = 668 2.2 us, with a load per code
+// 6.9.
 __device__ __forceinline__ uint4 load_last_codes(const int8_t* p, int n) {
+  uint4 whole = make_uint4(0u, 0u, 0u, 0u);
+  if (n >= 16) whole = ldg_stream(p);
+  const int r = n >= 16 ? 0 : max(n, 0);
   uint2 lo = make_uint2(0u, 0u);
   uint64_t b4 = 0, b2 = 0, b1 = 0;
-  if (n & 8) lo = *reinterpret_cast<const uint2*>(p);
-  if (n & 4) b4 = *reinterpret_cast<const uint32_t*>(p + (n & 8));
-  if (n & 2) b2 = *reinterpret_cast<const uint16_t*>(p + (n & 12));
-  if (n & 1) b1 = *reinterpret_cast<const uint8_t*>(p + (n & 14));
-  const uint64_t t = b4 | b2 << (8 * (n & 4)) | b1 << (8 * (n & 6));
+  if (r & 8) lo = *reinterpret_cast<const uint2*>(p);
+  if (r & 4) b4 = *reinterpret_cast<const uint32_t*>(p + (r & 8));
+  if (r & 2) b2 = *reinterpret_cast<const uint16_t*>(p + (r & 12));
+  if (r & 1) b1 = *reinterpret_cast<const uint8_t*>(p + (r & 14));
+  const uint64_t t = b4 | b2 << (8 * (r & 4)) | b1 << (8 * (r & 6));
   const uint32_t t0 = (uint32_t)t, t1 = (uint32_t)(t >> 32);
-  return n & 8 ? make_uint4(lo.x, lo.y, t0, t1) : make_uint4(t0, t1, 0u, 0u);
+  if (n >= 16) return whole;
+  return r & 8 ? make_uint4(lo.x, lo.y, t0, t1) : make_uint4(t0, t1, 0u, 0u);
 }
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -204,8 +184,10 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 // 4096, replayed back to back, N = 4096 4.8 us (a block per tile 5.3, without the
 // hint 6.1), N = 10240 9.3 (a block per tile 12.6).  Three blocks per SM (two from 9
 // tokens on, whose fragments need the registers) leave room for the next kernel's
-// blocks, whose hints then run under this one.
-template <int NB, class O>
+// blocks, whose hints then run under this one.  TAIL: K is not a multiple of 64 (a
+// kernel of its own, as the last step's code costs the others 0.3 us of fetches and
+// registers).
+template <int NB, class O, bool TAIL>
 __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_kernel(Matmul8Args p) {
   constexpr int U = NB <= 2 ? 4 : 2;   // k steps (64 codes) in flight per warp
   __shared__ int part[2][kFewWarps][8 * NB][kFewRows + 1];
@@ -221,7 +203,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
   hint(blockIdx.x);
   grid_dependency_wait();
   grid_launch_dependents();
-  const int steps = (p.K + 63) / 64;
+  const int steps = p.K / 64;      // whole ones
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   int buf = 0;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
@@ -235,8 +217,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
       uint4 a[U][2], b[U][NB];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        const bool go = s0 + u * kFewWarps < steps;
         const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
-        const bool go = k0 + 16 <= p.K;
         a[u][0] = go && in0 ? ldg_stream(w0 + k0) : zero;
         a[u][1] = go && in1 ? ldg_stream(w1 + k0) : zero;
       }
@@ -245,7 +227,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
         const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
 #pragma unroll
         for (int i = 0; i < NB; ++i)
-          b[u][i] = k0 + 16 <= p.K && 8 * i + g < p.M
+          b[u][i] = s0 + u * kFewWarps < steps && 8 * i + g < p.M
                         ? *reinterpret_cast<const uint4*>(p.A + (int64_t)(8 * i + g) * p.lda + k0)
                         : zero;
       }
@@ -257,14 +239,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
           mma_s8(acc[i], a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u][i].z, b[u][i].w);
         }
     }
-    if (const int last = p.K % 16; last != 0 && warp == steps % kFewWarps) {   // the lanes that own its 16 codes
-      const int k0 = p.K - last;
-      const bool own = t == k0 / 16 % 4;
-      const uint4 a0 = load_last_codes(w0 + k0, own && in0 ? last : 0), a1 = load_last_codes(w1 + k0, own && in1 ? last : 0);
+    if (TAIL && warp == steps % kFewWarps) {
+      const int k0 = steps * 64 + 16 * t, n = p.K - k0;
+      const uint4 a0 = load_last_codes(w0 + k0, in0 ? n : 0), a1 = load_last_codes(w1 + k0, in1 ? n : 0);
       uint4 b[NB];
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
-        b[i] = load_last_codes(p.A + (int64_t)(8 * i + g) * p.lda + k0, own && 8 * i + g < p.M ? last : 0);
+      for (int i = 0; i < NB; ++i) b[i] = load_last_codes(p.A + (int64_t)(8 * i + g) * p.lda + k0, 8 * i + g < p.M ? n : 0);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         mma_s8(acc[i], a0.x, a1.x, a0.y, a1.y, b[i].x, b[i].y);
@@ -480,12 +460,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int tm, tn;
     tile_at(t0, pl, tm, tn);
     sm0 = (int64_t)tm * 2 * BM + (int64_t)half * BM;
-    sn0 = (int64_t)tn * BN;
+    sn0 = (int64_t)tn * BN + lane * 4;
 #pragma unroll
     for (int c = 0; c < kG; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t n = sn0 + c * 128 + lane_col(p.vec_out, lane, j);
+        const int64_t n = sn0 + c * 128 + j;
         const auto* bias = static_cast<const typename O::elem*>(p.bias);
         ssw[c][j] = n < p.N ? p.b_scale[n] : 0.0f;
         sbs[c][j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
@@ -726,7 +706,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < kG; ++c)
             if (q < S && (h == 0 || two))
-              v[h][q][c] = ld_row4(peer[q] + (uint32_t)((r + h * step) * C::kPartPitch + c * 512), lane, p.vec_out, true);
+              v[h][q][c] = ld_cluster_v4(peer[q] + (uint32_t)((r + h * step) * C::kPartPitch + (c * 128 + lane * 4) * 4));
 #pragma unroll
       for (int h = 0; h < kRows; ++h) {
         if (h == 1 && !two) break;
@@ -742,11 +722,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               a[3] += (int)v[h][q][c].w;
             }
           const int64_t n = n0 + c * 128;
+          if (n >= p.N) continue;
           const bool hb = p.bias != nullptr;
           float y[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], sx[h], ssw[c][j], p.inv_group, sbs[c][j], hb);
-          store_row4<O>(static_cast<typename O::elem*>(p.Y) + (m0 + r + h * step) * p.ldy + n, p.N - n, lane, p.vec_out, y);
+          store4<O>(static_cast<typename O::elem*>(p.Y) + (m0 + r + h * step) * p.ldy + n, (int)min((int64_t)4, p.N - n),
+                    p.vec_out, y);
         }
       }
     }
@@ -892,14 +874,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   }
 
   // What the final step needs from global memory, while the products run.
-  const int64_t n0 = (int64_t)tile * kStreamRows;
+  const int64_t n = (int64_t)tile * kStreamRows + 4 * lane;
   const auto* bias = static_cast<const typename O::elem*>(p.bias);
   float sw[4], bs[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int64_t n = n0 + lane_col(p.vec_out, lane, j);
-    sw[j] = n < p.N ? p.b_scale[n] : 0.0f;
-    bs[j] = bias && n < p.N ? O::to(bias[n]) : 0.0f;
+    sw[j] = n + j < p.N ? p.b_scale[n + j] : 0.0f;
+    bs[j] = bias && n + j < p.N ? O::to(bias[n + j]) : 0.0f;
   }
   if (threadIdx.x >= 64 && threadIdx.x < 64 + NT) {    // warps 2 to 5
     const int m = (int)threadIdx.x - 64;
@@ -934,10 +915,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll
   for (int r = 0; r < 8; ++r) peer[r] = split > 1 && r < split ? map_to_rank(base, (uint32_t)r) : base;
   for (int m = q + warp * split; m < tokens; m += (kStreamThreads / 32) * split) {
-    const uint32_t at = (uint32_t)(m * C::kPartPitch);
+    const uint32_t at = (uint32_t)(m * C::kPartPitch + 16 * lane);
     int a[4];
     if (split == 1) {
-      const uint4 v = ld_row4(base + at, lane, p.vec_out, false);
+      const uint4 v = ld_shared_v4(base + at);
       a[0] = (int)v.x;
       a[1] = (int)v.y;
       a[2] = (int)v.z;
@@ -946,7 +927,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       uint4 v[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r)
-        if (r < split) v[r] = ld_row4(peer[r] + at, lane, p.vec_out, true);
+        if (r < split) v[r] = ld_cluster_v4(peer[r] + at);
       a[0] = a[1] = a[2] = a[3] = 0;
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -957,11 +938,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           a[3] += (int)v[r].w;
         }
     }
-    const float s = sx[m];
-    float y[4];
+    if (n < p.N) {
+      const float s = sx[m];
+      float y[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], s, sw[j], p.inv_group, bs[j], bias != nullptr);
-    store_row4<O>(static_cast<typename O::elem*>(p.Y) + (int64_t)(m0 + m) * p.ldy + n0, p.N - n0, lane, p.vec_out, y);
+      for (int j = 0; j < 4; ++j) y[j] = dequant(a[j], s, sw[j], p.inv_group, bs[j], bias != nullptr);
+      store4<O>(static_cast<typename O::elem*>(p.Y) + (int64_t)(m0 + m) * p.ldy + n, (int)min((int64_t)4, p.N - n),
+                p.vec_out, y);
+    }
   }
   if (split > 1) cluster_sync();                       // the sums stay readable until every CTA has taken them
   if (warp == 2) {
@@ -1018,7 +1002,8 @@ cudaError_t launch_few(const Matmul8Args& a, int sms, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_tokens_kernel<NB, O>, a);
+  return a.K % 64 ? cudaLaunchKernelEx(&cfg, few_tokens_kernel<NB, O, true>, a)
+                  : cudaLaunchKernelEx(&cfg, few_tokens_kernel<NB, O, false>, a);
 }
 
 // How many clusters of `size` CTAs of a kernel fit on the device at once (0
