@@ -181,8 +181,8 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 // in flight, and a tile's weights are asked into L2 a tile ahead, the first one's
 // before the wait for the previous kernel (a hint; the loads after the wait read
 // memory as it then is).  Resident blocks take the tiles in turn: one token, K =
-// 4096, replayed back to back, N = 4096 4.8 us (a block per tile 5.3, without the
-// hint 6.1), N = 10240 9.3 (a block per tile 12.6).  Three blocks per SM (two from 9
+// 4096, replayed back to back, N = 4096 4.6 us (every load under its predicate 5.1, a
+// block per tile 5.3, without the hint 6.1), N = 10240 8.8 (a block per tile 12.6).  Three blocks per SM (two from 9
 // tokens on, whose fragments need the registers) leave room for the next kernel's
 // blocks, whose hints then run under this one.  TAIL: K is not a multiple of 64 (a
 // kernel of its own, as the last step's code costs the others 0.3 us of fetches and
@@ -209,27 +209,28 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
     if (tile + gridDim.x < tiles) hint(tile + gridDim.x);
     const int64_t n0 = tile * kFewRows;
-    const bool in0 = n0 + g < p.N, in1 = n0 + g + 8 < p.N;
-    const int8_t* w0 = p.B + (n0 + g) * p.ldb;
-    const int8_t* w1 = p.B + (n0 + g + 8) * p.ldb;
+    // Channels and tokens past the ends read row 0 instead; their sums go nowhere.
+    const int8_t* w0 = p.B + (n0 + g < p.N ? n0 + g : 0) * p.ldb + 16 * t;
+    const int8_t* w1 = p.B + (n0 + g + 8 < p.N ? n0 + g + 8 : 0) * p.ldb + 16 * t;
+    const int8_t* x[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) x[i] = p.A + (8 * i + g < p.M ? 8 * i + g : 0) * p.lda + 16 * t;
     int acc[NB][4] = {};
-    for (int s0 = warp; s0 < steps; s0 += kFewWarps * U) {
+    auto round = [&](int s0, auto full) {              // steps s0, s0 + 8, ...: U of them, or those that there are
       uint4 a[U][2], b[U][NB];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool go = s0 + u * kFewWarps < steps;
-        const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
-        a[u][0] = go && in0 ? ldg_stream(w0 + k0) : zero;
-        a[u][1] = go && in1 ? ldg_stream(w1 + k0) : zero;
+        const bool go = decltype(full)::value || s0 + u * kFewWarps < steps;
+        const int k0 = (s0 + u * kFewWarps) * 64;
+        a[u][0] = go ? ldg_stream(w0 + k0) : zero;
+        a[u][1] = go ? ldg_stream(w1 + k0) : zero;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k0 = (s0 + u * kFewWarps) * 64 + 16 * t;
+        const bool go = decltype(full)::value || s0 + u * kFewWarps < steps;
+        const int k0 = (s0 + u * kFewWarps) * 64;
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-          b[u][i] = s0 + u * kFewWarps < steps && 8 * i + g < p.M
-                        ? *reinterpret_cast<const uint4*>(p.A + (int64_t)(8 * i + g) * p.lda + k0)
-                        : zero;
+        for (int i = 0; i < NB; ++i) b[u][i] = go ? *reinterpret_cast<const uint4*>(x[i] + k0) : zero;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -238,13 +239,16 @@ __global__ void __launch_bounds__(kFewWarps * 32, NB == 1 ? 3 : 2) few_tokens_ke
           mma_s8(acc[i], a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u][i].x, b[u][i].y);
           mma_s8(acc[i], a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u][i].z, b[u][i].w);
         }
-    }
+    };
+    int s0 = warp;
+    for (; s0 + (U - 1) * kFewWarps < steps; s0 += kFewWarps * U) round(s0, std::true_type{});
+    if (s0 < steps) round(s0, std::false_type{});
     if (TAIL && warp == steps % kFewWarps) {
-      const int k0 = steps * 64 + 16 * t, n = p.K - k0;
-      const uint4 a0 = load_last_codes(w0 + k0, in0 ? n : 0), a1 = load_last_codes(w1 + k0, in1 ? n : 0);
+      const int n = p.K - steps * 64 - 16 * t;
+      const uint4 a0 = load_last_codes(w0 + steps * 64, n), a1 = load_last_codes(w1 + steps * 64, n);
       uint4 b[NB];
 #pragma unroll
-      for (int i = 0; i < NB; ++i) b[i] = load_last_codes(p.A + (int64_t)(8 * i + g) * p.lda + k0, 8 * i + g < p.M ? n : 0);
+      for (int i = 0; i < NB; ++i) b[i] = load_last_codes(x[i] + steps * 64, n);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         mma_s8(acc[i], a0.x, a1.x, a0.y, a1.y, b[i].x, b[i].y);
@@ -1151,8 +1155,8 @@ cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
   // Few tokens.  Up to 8, with 44 MB of weights and 8192 codes of k at most (us
-  // against the best streamed form, 8 tokens): 4096 x 4096 5.1 (6.6), 10240 x 4096 10.2
-  // (12.0), 14336 x 4096 14.1 (13.4), 4096 x 8192 9.6 (9.9), 4096 x 14336 14.6 (13.1, one
+  // against the best streamed form, 8 tokens): 4096 x 4096 5.1 (6.6), 10240 x 4096 9.6
+  // (12.0), 14336 x 4096 14.1 (13.4), 4096 x 8192 9.0 (9.9), 4096 x 14336 14.6 (13.1, one
   // token).  Up to 16, with every tile resident at once: 4096 x 4096 5.7 (6.7), 1024 x
   // 1024 2.2 (4.0), 6144 x 4096 10.0 (8.8), 1024 x 16384 11.3 (9.0).  Up to 32, with
   // 2048 codes besides: 1024 x 1024 2.6 (4.3), 4096 x 2048 5.1 (5.3), 1024 x 4096 5.6
