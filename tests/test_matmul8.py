@@ -115,6 +115,7 @@ def test_product(M, N, K, group, dtype):
 FEW_SHAPES = [                                               # on both sides of the few-token forms' limits
     (1, 7200, 100, 0), (5, 14500, 333, 128), (8, 21500, 2000, 0), (7, 200, 8192, 0), (7, 200, 8193, 0), (2, 22600, 2048, 0),
     (9, 4736, 65, 0), (9, 4737, 65, 0), (13, 4700, 1000, 64), (16, 300, 8192, 0), (16, 300, 8208, 0), (12, 17, 30, 0),
+    (3, 500, 16384, 0), (3, 500, 16385, 0), (32, 500, 4096, 0), (32, 500, 4097, 0),
     (17, 4736, 50, 0), (25, 4737, 500, 0), (31, 1000, 2047, 0), (32, 1000, 2049, 0), (32, 15, 2048, 128), (20, 9, 1, 0),
 ]
 

@@ -1154,17 +1154,17 @@ cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
-  // Few tokens.  Up to 8, with 44 MB of weights and 8192 codes of k at most (us
-  // against the best streamed form, 8 tokens): 4096 x 4096 5.1 (6.6), 10240 x 4096 9.6
-  // (12.0), 14336 x 4096 14.1 (13.4), 4096 x 8192 9.0 (9.9), 4096 x 14336 14.6 (13.1, one
-  // token).  Up to 16, with every tile resident at once: 4096 x 4096 5.7 (6.7), 1024 x
-  // 1024 2.2 (4.0), 6144 x 4096 10.0 (8.8), 1024 x 16384 11.3 (9.0).  Up to 32, with
-  // 2048 codes besides: 1024 x 1024 2.6 (4.3), 4096 x 2048 5.1 (5.3), 1024 x 4096 5.6
-  // (5.1).
+  // Few tokens (us against the best streamed form).  Up to 8, with 52 MB of weights and
+  // 8192 codes of k, or 16 MB and 16384, at most; 8 tokens: 4096 x 4096 5.1 (6.6), 12288 x
+  // 4096 10.4 (12.4), 14336 x 4096 13.4 (13.2), 6144 x 8192 9.3 (12.9), 8192 x 8192 16.8
+  // (14.5), 1024 x 16384 8.7 (9.0), 4096 x 12288 12.8 (11.4).  Up to 16, with 8192 codes and
+  // every tile resident at once: 4096 x 4096 5.2 (6.7), 1024 x 1024 2.2 (4.0), 4736 x 8192
+  // 8.8 (12.1), 14336 x 1024 6.4 (6.1).  Up to 32, with 4096 codes besides: 1024 x 1024 2.6
+  // (4.3), 4096 x 4096 6.7 (6.9), 2048 x 8192 9.5 (7.5).
   const bool resident = a.N <= 2 * sms * kFewRows;
-  if (a.M <= 8 && a.K <= 8192 && (int64_t)a.N * a.K <= (int64_t)44 << 20) return launch_few<1, O>(a, sms, st);
+  if (a.M <= 8 && a.K <= 16384 && (int64_t)a.N * a.K <= (int64_t)(a.K <= 8192 ? 52 : 16) << 20) return launch_few<1, O>(a, sms, st);
   if (a.M <= 16 && a.K <= 8192 && resident) return launch_few<2, O>(a, sms, st);
-  if (a.M <= 32 && a.K <= 2048 && resident) return launch_few<4, O>(a, sms, st);
+  if (a.M <= 32 && a.K <= 4096 && resident) return launch_few<4, O>(a, sms, st);
   Form f{0, 0, 0, 1e30f};
   if (a.M <= 16) consider_streamed<16, O>(a, sms, dev, f);
   else if (a.M <= 32) consider_streamed<32, O>(a, sms, dev, f);
