@@ -198,6 +198,7 @@ w4a4_status w8a8_linear(const void* X, const int8_t* Wq, const float* w_scale, i
  *     not looked at when its matrix has one row.
  *   - Activation tensors need the alignment of their element only; 16-byte
  *     aligned bases and strides (in bytes) with K a multiple of 8 run faster.
+ *     Bytes between the rows of an input may be read, and are not used.
  *     Code tensors (int8) need 16-byte-aligned bases and strides that are
  *     multiples of 16; the bytes between K and the stride are neither read
  *     nor written.
