@@ -214,9 +214,9 @@ typedef enum { W4A4_DTYPE_BF16 = 0, W4A4_DTYPE_FP16 = 1, W4A4_DTYPE_FP32 = 2 } w
  *   per group of `group`: y <- H_g y (group 0: none),
  *   x_scale = fl32(max |y| / 127), Xq = rint_half_even(y / x_scale),
  * and, where H is given, H = h rounded to the type.  The norm uses the
- * unrounded h, and y is not rounded before it is quantized.  The quotient is
- * formed with the reciprocal of x_scale in fp32: one within 127 * 2^-22 of a half
- * may go to the other side (y itself is known to about 20 * 2^-24 of its value).
+ * unrounded h, and y is not rounded before it is quantized.  The quotient q is
+ * formed with the reciprocal of x_scale in fp32: one within |q| * 1.01 * 2^-24 of a
+ * half may go to the other side (y itself is known to about 20 * 2^-24 of its value).
  *   X [M, K], residual [M, K] or NULL, gamma [K] or NULL, H [M, K] or NULL:
  *   `dtype`.  H may be X or residual itself (same base and stride), or share
  *   no byte with them; Xq and x_scale share no byte with any input.

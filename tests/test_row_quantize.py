@@ -501,3 +501,29 @@ def test_repeated_calls_are_bit_equal():
     for _ in range(5):
         again = w4.w8a8_add_rmsnorm_quantize(X, None, EPS, 128, residual=R)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+@gpu
+@pytest.mark.parametrize("M,K", [(2000, 384), (40, 4093)])
+def test_codes_next_to_a_half(M, K):
+    """Rows y = 32 up (SiLU(32) = 32 in fp32: 1 + e^-32 rounds to 1) whose values lie one to
+    three fp32 steps on either side of (k + 1/2) s.  The product y (1 / s) is rounded to an
+    integer without an intermediate rounding, and 1 / s is off by 1.01 u of itself, so every
+    quotient farther than that from its half has one code only."""
+    import torch
+    rng = np.random.default_rng(90)
+    m = (1.0 + rng.random(M)).astype(np.float32)
+    s = (m / np.float32(127.0)).astype(np.float32)
+    half = (rng.integers(0, 126, (M, K)) + 0.5) * s.astype(np.float64)[:, None]
+    y = half.astype(np.float32)
+    y = y.view(np.int32) + rng.integers(-3, 4, (M, K)).astype(np.int32)
+    y = y.view(np.float32) * np.where(rng.random((M, K)) < 0.5, -1, 1).astype(np.float32)
+    y[:, K // 2] = m
+    up = torch.from_numpy(y / np.float32(32.0)).cuda()
+    q, got = w4.w8a8_silu_mul_quantize(torch.full_like(up, 32.0), up)
+    torch.cuda.synchronize()
+    assert np.array_equal(got.cpu().numpy(), s)
+    r = y.astype(np.float64) / s.astype(np.float64)[:, None]
+    apart = np.abs(np.abs(r) - np.floor(np.abs(r)) - 0.5) > 1.01 * U * np.abs(r)
+    assert 0.5 < apart.mean() < 1.0
+    assert np.array_equal(q.cpu().numpy()[apart], np.rint(r)[apart].astype(np.int8))

@@ -5,8 +5,8 @@
 //          between the two products of a gated MLP)
 // then, per row and as in the rotate + quantize path: y <- H_g y per group of
 // g (fp32 butterflies in the order h = 1, 2, 4, ...; g = 0: none), s =
-// fl32(max |y| / 127), q = rint_half_even(y / s) with 1 / s by the hardware's
-// reciprocal, codes 0 where s = 0.
+// fl32(max |y| / 127), q = rint_half_even(y / s) with 1 / s within one rounding
+// of fp32, codes 0 where s = 0.
 //
 // Everything between the loads and the codes is fp32 in registers: h is not
 // rounded to the tensors' type before the norm (only the stored sum is), and
@@ -253,8 +253,9 @@ __device__ __forceinline__ uint32_t pack_bytes4(uint32_t t0, uint32_t t1, uint32
 }
 
 // Codes of 8 elements: each times 1 / s (`inv`), rounded to the nearest integer
-// by adding 1.5 * 2^23 in one fused operation.  A quotient within 127 * 2^-22 of
-// a half may go to the other side; y itself is known no better than that.
+// by adding 1.5 * 2^23 in one fused operation.  inv is off by at most 1.01 * 2^-24
+// of itself, so a quotient q within |q| * 1.01 * 2^-24 of a half may go to the
+// other side; y itself is known no better than that.
 __device__ __forceinline__ uint2 quantize8(const float2 (&f)[4], float inv) {
   const float2 mg = make_float2(kMagic, kMagic), iv = make_float2(inv, inv);
   uint32_t t[8];
@@ -381,8 +382,13 @@ __device__ __forceinline__ void quantize_row(float2 (&f)[VPT][4], const RowQuant
   // Codes are 0 in a row of zeros and in one whose scale is NaN.
   const bool some = s > 0.0f;
   const uint32_t keep = some ? 0xFFFFFFFFu : 0u;
+  // The hardware's reciprocal (1 ulp, so codes next to a half by up to |q| 2^-23) and a
+  // Newton step: r (1 + e) -> r (1 - e^2), then one rounding.  Per row and thread: norm
+  // 16384 x 8192 bf16 157.1 -> 157.4 us, SiLU 8 x 14336 3.1 -> 3.2.
+  const float div = some && s >= 0x1p-100f ? s : 1.0f;
   float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(some && s >= 0x1p-100f ? s : 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(div));
+  inv = fmaf(inv, fmaf(-div, inv, 1.0f), inv);
   if (some && s < 0x1p-100f) {     // too small for its reciprocal, and of few bits itself where it is subnormal
     scale_row(f, 0x1p80f);
     const float big = s * 0x1p80f, top = 127.0f * big;
