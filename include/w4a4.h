@@ -229,8 +229,7 @@ w4a4_status w8a8_add_rmsnorm_quantize(const void* X, int64_t ldx, const void* re
                                       w4a4_stream_t stream);
 
 /* SiLU(gate) * up, rotation, int8 quantization:
- *   y = (gate / (1 + exp(-gate))) * up (fp32), then as above.  Gates below -87
- *   count as 0 (the function is under 1.2e-36 there).
+ *   y = (gate / (1 + exp(-gate))) * up (fp32), then as above.
  *   gate, up [M, K]: `dtype`; the two halves of one [M, 2 K] product are
  *   given as two pointers with the same stride.  Shapes as above. */
 w4a4_status w8a8_silu_mul_quantize(const void* gate, int64_t ldg, const void* up, int64_t ldu, int M, int K,

@@ -10,8 +10,9 @@ Tolerances, with u = 2^-24 (half a step of fp32, relative):
   silu  t = 2^(-a log2 e): the exponent's two roundings put 1.5 |a| u into t and
         ex2.approx 4 u, of which t / (1 + t) reaches y: for a >= 0 at most 2 u +
         0.5 u, for a < 0 all of it; 1 + t (1 u), rcp.approx 1 ulp (2 u), two
-        products (2 u): at most 9 u + 1.5 max(0, -a) u of |y|.  Gates below -87
-        count as 0.
+        products (2 u): at most 9 u + 1.5 max(0, -a) u of |y|.  Below a = -87
+        four powers e^(a / 4) take the place of t: 1.22 |a| u from their exponents,
+        16 u of their own and 11 u of the rest, under the same sum.
   rotation  a sum of g values in log2 g roundings: at most (c + log2 g) u of
         the group's sum of |y|.
 With D the largest such error of a row, the scale is off by at most
@@ -527,3 +528,26 @@ def test_codes_next_to_a_half(M, K):
     apart = np.abs(np.abs(r) - np.floor(np.abs(r)) - 0.5) > 1.01 * U * np.abs(r)
     assert 0.5 < apart.mean() < 1.0
     assert np.array_equal(q.cpu().numpy()[apart], np.rint(r)[apart].astype(np.int8))
+
+
+@gpu
+@pytest.mark.parametrize("M,K,pad", [(40, 64, 0), (300, 1000, 0), (300, 1001, 1), (4000, 3200, 0), (1500, 6001, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_large_values_behind_strongly_negative_gates(M, K, pad, dtype):
+    """silu(-100) = -3.7e-42 leaves fp32's normal range, times 1e38 it does not: each row has gates
+    around one of -80 to -170 and values up to the type's largest."""
+    import torch
+    dt = _dt(dtype)
+    rng = np.random.default_rng(91)
+    base = rng.uniform(-170.0, -80.0, (M, 1))
+    gate = _rows(base + rng.uniform(-4.0, 4.0, (M, K)), dt, pad)
+    up = _rows(rng.choice([-1.0, 1.0], (M, K)) * np.exp(rng.uniform(80.0, 88.0, (M, K))), dt, pad)
+    gate[:, 1], up[:, 1] = torch.finfo(dt).min, 1.0
+    q, s = w4.w8a8_silu_mul_quantize(gate, up)
+    torch.cuda.synchronize()
+    a, b = _f64(gate), _f64(up)
+    with np.errstate(over="ignore"):
+        y, c = silu64(a, b), silu_c(np.maximum(a, -200.0))
+    y[:, 1] = 0.0
+    assert (np.abs(y).max(axis=1) > 2.0 ** -126).all()
+    check_codes(y, 0, c, _f64(q), _f64(s))
