@@ -551,3 +551,31 @@ def test_large_values_behind_strongly_negative_gates(M, K, pad, dtype):
     y[:, 1] = 0.0
     assert (np.abs(y).max(axis=1) > 2.0 ** -126).all()
     check_codes(y, 0, c, _f64(q), _f64(s))
+
+
+@pytest.mark.parametrize("group", [1 << 32, (1 << 32) + 64, -(1 << 32), -1, 1 << 31])
+def test_marshalling_refuses_a_group_that_is_no_int(lib, group):
+    """Before anything else is looked at: the low 32 bits of these are groups that the library takes."""
+    import torch
+    w4._bind_calls()
+    x, q, s = torch.zeros(2, 64), torch.zeros((2, 64), dtype=torch.int8), torch.zeros(2)
+    c = w4._calls
+    assert c.add_rmsnorm_quantize(x, None, EPS, group, None, None, q, s, 0) == SHAPE
+    assert c.silu_mul_quantize(x, x, group, q, s, 0) == SHAPE
+    assert c.matmul(q, s, q, s, group, None, x, 0) == SHAPE
+    assert c.silu_mul_quantize(x, x, 64, q, s, 0) == INVALID      # host tensors
+    with pytest.raises(TypeError):
+        c.silu_mul_quantize(x, x, 64.0, q, s, 0)
+
+
+@gpu
+@pytest.mark.parametrize("group", [1 << 32, (1 << 32) + 64])
+def test_a_group_past_32_bits_is_refused(group):
+    import torch
+    X = torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")
+    q, s = torch.zeros((4, 128), dtype=torch.int8, device="cuda"), torch.zeros(4, device="cuda")
+    for call in (lambda: w4.w8a8_add_rmsnorm_quantize(X, None, EPS, group), lambda: w4.w8a8_silu_mul_quantize(X, X, group),
+                 lambda: w4.w8a8_matmul(q, s, q, s, group)):
+        with pytest.raises(w4.W4A4Error) as e:
+            call()
+        assert e.value.status == SHAPE

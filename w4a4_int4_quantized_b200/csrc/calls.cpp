@@ -56,61 +56,68 @@ int vector(PyObject* o, int64_t n, at::ScalarType type, int64_t dev, void** p) {
 
 bool fits_int(int64_t v) { return v >= 0 && v <= 0x7FFFFFFF; }
 
+// An int argument; what does not fit one is no shape that the library takes.
+int integer(PyObject* o, int& v) {
+  const long l = PyLong_AsLong(o);
+  if (l == -1 && PyErr_Occurred()) return -1;
+  if (!fits_int(l)) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  v = (int)l;
+  return W4A4_OK;
+}
+
 // (X, gamma, eps, group, residual, H, Xq, x_scale, stream)
 int norm(PyObject* const* a) {
+  int group = 0, e;
+  const double eps = PyFloat_AsDouble(a[2]);
+  if ((eps == -1.0 && PyErr_Occurred()) || (e = integer(a[3], group)) < 0) return -1;
+  if (e != 0) return e;
   const at::Tensor* X = tensor(a[0]);
   if (!X || X->dim() != 2 || !X->is_cuda()) return W4A4_ERR_INVALID_ARG;
   const int64_t M = X->size(0), K = X->size(1), dev = X->get_device();
   const at::ScalarType type = X->scalar_type();
   if (!fits_int(M) || !fits_int(K)) return W4A4_ERR_UNSUPPORTED_SHAPE;
-  const double eps = PyFloat_AsDouble(a[2]);
-  const long group = PyLong_AsLong(a[3]);
-  if (PyErr_Occurred()) return -1;
   Mat x, r, h, q;
   void *g = nullptr, *s = nullptr;
-  int e;
   if ((e = matrix(a[0], M, K, type, dev, x)) != 0) return e;
   if (a[4] != Py_None && (e = matrix(a[4], M, K, type, dev, r)) != 0) return e;
   if (a[1] != Py_None && (e = vector(a[1], K, type, dev, &g)) != 0) return e;
   if (a[5] != Py_None && (e = matrix(a[5], M, K, type, dev, h)) != 0) return e;
   if ((e = matrix(a[6], M, K, at::kChar, dev, q)) != 0) return e;
   if ((e = vector(a[7], M, at::kFloat, dev, &s)) != 0) return e;
-  return g_norm(x.p, x.ld, r.p, r.ld, g, (float)eps, (int)M, (int)K, (int)group, dtype_of(*X), h.p, h.ld,
+  return g_norm(x.p, x.ld, r.p, r.ld, g, (float)eps, (int)M, (int)K, group, dtype_of(*X), h.p, h.ld,
                 static_cast<int8_t*>(q.p), q.ld, static_cast<float*>(s),
                 static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[8])));
 }
 
 // (gate, up, group, Xq, x_scale, stream)
 int silu(PyObject* const* a) {
+  int group = 0, e;
+  if ((e = integer(a[2], group)) != 0) return e;
   const at::Tensor* G = tensor(a[0]);
   if (!G || G->dim() != 2 || !G->is_cuda()) return W4A4_ERR_INVALID_ARG;
   const int64_t M = G->size(0), K = G->size(1), dev = G->get_device();
   if (!fits_int(M) || !fits_int(K)) return W4A4_ERR_UNSUPPORTED_SHAPE;
-  const long group = PyLong_AsLong(a[2]);
-  if (PyErr_Occurred()) return -1;
   Mat g, u, q;
   void* s = nullptr;
-  int e;
   if ((e = matrix(a[0], M, K, G->scalar_type(), dev, g)) != 0) return e;
   if ((e = matrix(a[1], M, K, G->scalar_type(), dev, u)) != 0) return e;
   if ((e = matrix(a[3], M, K, at::kChar, dev, q)) != 0) return e;
   if ((e = vector(a[4], M, at::kFloat, dev, &s)) != 0) return e;
-  return g_silu(g.p, g.ld, u.p, u.ld, (int)M, (int)K, (int)group, dtype_of(*G), static_cast<int8_t*>(q.p), q.ld,
+  return g_silu(g.p, g.ld, u.p, u.ld, (int)M, (int)K, group, dtype_of(*G), static_cast<int8_t*>(q.p), q.ld,
                 static_cast<float*>(s), static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[5])));
 }
 
 // (Xq, x_scale, Wq, w_scale, group, bias, Y, stream)
 int matmul(PyObject* const* a) {
+  int group = 0, e;
+  if ((e = integer(a[4], group)) != 0) return e;
   const at::Tensor *X = tensor(a[0]), *W = tensor(a[2]), *Y = tensor(a[6]);
   if (!X || !W || !Y || X->dim() != 2 || W->dim() != 2 || !X->is_cuda()) return W4A4_ERR_INVALID_ARG;
   const int64_t M = X->size(0), K = X->size(1), N = W->size(0), dev = X->get_device();
   if (!fits_int(M) || !fits_int(K) || !fits_int(N)) return W4A4_ERR_UNSUPPORTED_SHAPE;
-  const long group = PyLong_AsLong(a[4]);
-  if (PyErr_Occurred()) return -1;
   const at::ScalarType type = Y->scalar_type();
   Mat x, w, y;
   void *sx = nullptr, *sw = nullptr, *b = nullptr;
-  int e;
   if ((e = matrix(a[0], M, K, at::kChar, dev, x)) != 0) return e;
   if ((e = matrix(a[2], N, K, at::kChar, dev, w)) != 0) return e;
   if ((e = vector(a[1], M, at::kFloat, dev, &sx)) != 0) return e;
@@ -119,7 +126,7 @@ int matmul(PyObject* const* a) {
   if ((e = matrix(a[6], M, N, type, dev, y)) != 0) return e;
   return g_matmul(static_cast<const int8_t*>(x.p), x.ld, static_cast<const float*>(sx),
                   static_cast<const int8_t*>(w.p), w.ld, static_cast<const float*>(sw), (int)M, (int)N, (int)K,
-                  (int)group, b, dtype_of(*Y), y.p, y.ld, static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[7])));
+                  group, b, dtype_of(*Y), y.p, y.ld, static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[7])));
 }
 
 template <int (*F)(PyObject* const*), Py_ssize_t ARGS>
