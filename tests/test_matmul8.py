@@ -361,3 +361,53 @@ def test_large_output_and_many_tiles():
     torch.cuda.synchronize()
     for rows in (slice(0, 40), slice(32990, 33030), slice(M - 40, M)):
         check_product(Y[rows], Xq[rows], sx[rows], Wq, sw, 0, v)
+
+
+_WAITING = r"""
+#include <unistd.h>
+static volatile int go = 0;
+extern "C" void let_go() { go = 1; }
+extern "C" int entry() {                  // stands in for an entry point whose launch waits
+  for (int i = 0; i < 3000 && !go; ++i) usleep(1000);
+  const int seen = go;
+  go = 0;
+  return seen ? 0 : 5;
+}
+"""
+
+_LOCK = """
+import ctypes, sys, threading, time
+import torch
+import w4a4_int4_quantized_b200 as w4
+lib = ctypes.CDLL(sys.argv[1])
+w4._bind_calls()
+at = ctypes.cast(lib.entry, ctypes.c_void_p).value
+w4._calls.bind(at, at, at)
+x = torch.zeros((2, 64), device="cuda")
+q, s = torch.zeros((2, 64), dtype=torch.int8, device="cuda"), torch.zeros(2, device="cuda")
+for call in (lambda: w4.w8a8_add_rmsnorm_quantize(x, None, 1e-6), lambda: w4.w8a8_silu_mul_quantize(x, x),
+             lambda: w4.w8a8_matmul(q, s, q, s)):
+    def other():
+        time.sleep(0.1)
+        lib.let_go()
+    t = threading.Thread(target=other)
+    t.start()
+    call()                                # raises where the other thread could not run
+    t.join()
+print("ran")
+"""
+
+
+@gpu
+def test_other_host_threads_run_while_a_call_waits(tmp_path):
+    """A call lets the interpreter lock go: what its launch waits for may need it.  The library's
+    entry points are replaced by a host function that waits; nothing is launched."""
+    import os
+    import subprocess
+    import sys
+    src, lib = tmp_path / "entry.cpp", tmp_path / "entry.so"
+    src.write_text(_WAITING)
+    subprocess.run(["g++", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _LOCK, str(lib)], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "ran" in r.stdout, r.stderr[-2000:]

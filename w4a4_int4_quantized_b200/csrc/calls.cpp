@@ -65,6 +65,14 @@ int integer(PyObject* o, int& v) {
   return W4A4_OK;
 }
 
+// The interpreter lock let go for the library's call, as ctypes does: a launch waits
+// where the stream's queue is full, and what it waits for may be a host function
+// that needs the lock.
+struct WithoutLock {
+  PyThreadState* state = PyEval_SaveThread();
+  ~WithoutLock() { PyEval_RestoreThread(state); }
+};
+
 // (X, gamma, eps, group, residual, H, Xq, x_scale, stream)
 int norm(PyObject* const* a) {
   int group = 0, e;
@@ -84,9 +92,11 @@ int norm(PyObject* const* a) {
   if (a[5] != Py_None && (e = matrix(a[5], M, K, type, dev, h)) != 0) return e;
   if ((e = matrix(a[6], M, K, at::kChar, dev, q)) != 0) return e;
   if ((e = vector(a[7], M, at::kFloat, dev, &s)) != 0) return e;
+  const auto stream = static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[8]));
+  if (PyErr_Occurred()) return -1;
+  const WithoutLock unlocked;
   return g_norm(x.p, x.ld, r.p, r.ld, g, (float)eps, (int)M, (int)K, group, dtype_of(*X), h.p, h.ld,
-                static_cast<int8_t*>(q.p), q.ld, static_cast<float*>(s),
-                static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[8])));
+                static_cast<int8_t*>(q.p), q.ld, static_cast<float*>(s), stream);
 }
 
 // (gate, up, group, Xq, x_scale, stream)
@@ -103,8 +113,11 @@ int silu(PyObject* const* a) {
   if ((e = matrix(a[1], M, K, G->scalar_type(), dev, u)) != 0) return e;
   if ((e = matrix(a[3], M, K, at::kChar, dev, q)) != 0) return e;
   if ((e = vector(a[4], M, at::kFloat, dev, &s)) != 0) return e;
+  const auto stream = static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[5]));
+  if (PyErr_Occurred()) return -1;
+  const WithoutLock unlocked;
   return g_silu(g.p, g.ld, u.p, u.ld, (int)M, (int)K, group, dtype_of(*G), static_cast<int8_t*>(q.p), q.ld,
-                static_cast<float*>(s), static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[5])));
+                static_cast<float*>(s), stream);
 }
 
 // (Xq, x_scale, Wq, w_scale, group, bias, Y, stream)
@@ -124,9 +137,12 @@ int matmul(PyObject* const* a) {
   if ((e = vector(a[3], N, at::kFloat, dev, &sw)) != 0) return e;
   if (a[5] != Py_None && (e = vector(a[5], N, type, dev, &b)) != 0) return e;
   if ((e = matrix(a[6], M, N, type, dev, y)) != 0) return e;
+  const auto stream = static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[7]));
+  if (PyErr_Occurred()) return -1;
+  const WithoutLock unlocked;
   return g_matmul(static_cast<const int8_t*>(x.p), x.ld, static_cast<const float*>(sx),
                   static_cast<const int8_t*>(w.p), w.ld, static_cast<const float*>(sw), (int)M, (int)N, (int)K,
-                  group, b, dtype_of(*Y), y.p, y.ld, static_cast<w4a4_stream_t>(PyLong_AsVoidPtr(a[7])));
+                  group, b, dtype_of(*Y), y.p, y.ld, stream);
 }
 
 template <int (*F)(PyObject* const*), Py_ssize_t ARGS>
