@@ -9,7 +9,7 @@ library is missing or a call fails, a ``W4A4Error`` is raised.
 
 The operators around the INT8 product (w8a8_add_rmsnorm_quantize,
 w8a8_silu_mul_quantize, w8a8_matmul) also take fp16 and fp32 and rows of any
-stride; their arguments are marshalled by _calls.so.
+stride; their arguments are marshalled in C++ (csrc/calls.cpp).
 
 bf16 tensors are torch.bfloat16; packed INT4 codes are torch.uint8 [rows, K/2];
 INT8 codes are torch.int8 [rows, K]; scales are torch.float32 [rows].
@@ -263,7 +263,7 @@ def w8a8_linear(X, Wq, w_scale, group, bias=None, Y=None, workspace=None, stream
 # ---- around the INT8 product: strided rows, three element types -------------
 #
 # A decoded token's kernels take 2 to 6 us, so what happens before the launch is
-# kept short: the tensors are checked and the C function is called in _calls.so,
+# kept short: the tensors are checked and the C function is called in calls.cpp,
 # and the common case (tensors of the current device, its current stream) needs
 # no context manager and no stream object.
 
@@ -271,14 +271,16 @@ _torch = _calls = _raw_stream = _cur_device = None
 
 
 def _bind_calls():
-    """Load _calls.so and give it the library's entry points."""
+    """Load the module of calls.cpp and give it the library's entry points."""
     global _torch, _calls, _raw_stream, _cur_device
     import importlib.machinery
     import importlib.util
 
     import torch
+
+    from .build import calls_path
     lib = load_library()
-    path = os.path.join(_HERE, "_calls.so")
+    path = calls_path()
     if not os.path.exists(path):
         raise W4A4Error("load_library", 4) from FileNotFoundError(
             f"{path} not built; run __graft_entry__.build() or python -m w4a4_int4_quantized_b200.build")

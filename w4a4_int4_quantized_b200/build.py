@@ -3,8 +3,9 @@
 Every translation unit under ``csrc/`` is compiled for ``sm_100a`` only (no
 PTX for other targets, no other architectures), then linked into one shared
 object next to this file, with the CUDA runtime linked statically so the
-library loads on hosts without a GPU.  ``_calls.so`` beside it (``calls.cpp``,
-g++ against torch's headers) marshals the arguments of the shortest calls.
+library loads on hosts without a GPU.  ``_calls.<torch>.<python>.so`` beside it
+(``calls.cpp``, g++ against torch's headers) marshals the arguments of the
+shortest calls; the C ABI needs neither it nor torch.
 """
 from __future__ import annotations
 
@@ -21,7 +22,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libw4a4.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
-CALLS = os.path.join(HERE, "_calls.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
@@ -61,15 +61,29 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
-def _build_calls(force: bool) -> None:
-    deps = [CALLS_SRC, os.path.join(INCLUDE, "w4a4.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(CALLS) and all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
-        return
+def calls_path() -> str:
+    """The marshalling module for the running torch and Python: it has torch's C++
+    tensor layout and CPython's API compiled in, so its name says which."""
     import sysconfig
 
     import torch
+    return os.path.join(HERE, f"_calls.torch-{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+def _build_calls(force: bool) -> None:
+    try:
+        import torch
+    except ImportError:
+        print("torch is not installed: the C ABI only, without the Python calls of calls.cpp", file=sys.stderr)
+        return
+    import sysconfig
+
+    path = calls_path()
+    deps = [CALLS_SRC, os.path.join(INCLUDE, "w4a4.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return
     root = os.path.dirname(torch.__file__)
-    tmp = CALLS + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
@@ -79,14 +93,11 @@ def _build_calls(force: bool) -> None:
            "-lc10", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+        raise RuntimeError(f"{cmd[0]} failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    _build_calls(force)
-    if not force and not _stale():
-        return LIB
+def _build_library(verbose_ptxas: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), _sources()))
@@ -97,6 +108,12 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    if force or _stale():
+        _build_library(verbose_ptxas)
+    _build_calls(force)
     return LIB
 
 
