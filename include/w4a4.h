@@ -381,6 +381,20 @@ w4a4_status w4a4_plan_rotate_quantize(int M, int K, int group, int sms, int resi
 w4a4_status w4a4_plan_gemm_split(int M, int N, int K, int rank, int sms, int clusters_of_8, int clusters_of_4,
                                  int* split);
 
+/* Host-only view of how w8a8_add_rmsnorm_quantize (silu == 0) and
+ * w8a8_silu_mul_quantize (silu != 0) are launched on a device with `sms` SMs, for
+ * tools and for tests that name the forms they cover: no CUDA call.  second: a
+ * residual is given (not looked at for silu, which has two inputs); aligned: every
+ * base and row stride is a multiple of 16 bytes.  Writes plan[5]:
+ *   plan[0]  0 rows read directly at 16-byte alignment, 1 by the granules around
+ *            them, 2 element by element (rows of one warp); 3 rows through a ring in
+ *            shared memory, every thread with whole chunks, 4 with threads that have
+ *            none, 5 off the alignment;
+ *   plan[1..3]  chunks of 8 elements per thread, threads per row, rows (or rings)
+ *            per block;  plan[4]  rows in flight in a ring, 0 without one.
+ * The pages have no counterpart. */
+w4a4_status w8a8_plan_rows(int silu, int second, int aligned, int M, int K, w4a4_dtype dtype, int sms, int* plan);
+
 /* ---------------------------------------------------------------- failures */
 /* Kernels never trap: a wait on another part of the kernel that runs past its
  * time limit (2 s) records a code in a per-device error word and lets the

@@ -478,6 +478,15 @@ w4a4_status w4a4_plan_gemm_split(int M, int N, int K, int rank, int sms, int clu
                                                                                   : W4A4_ERR_UNSUPPORTED_SHAPE;
 }
 
+w4a4_status w8a8_plan_rows(int silu, int second, int aligned, int M, int K, w4a4_dtype dtype, int sms, int* plan) {
+  if (!plan) return W4A4_ERR_INVALID_ARG;
+  const w4a4_status s = check_row_quantize(M, K, 0, dtype);
+  if (s != W4A4_OK) return s;
+  if (M < 1 || sms < 1) return W4A4_ERR_UNSUPPORTED_SHAPE;
+  plan_row_quantize(silu != 0, silu != 0 || second != 0, aligned != 0, (int)dtype, M, K, sms, plan);
+  return W4A4_OK;
+}
+
 // ------------------------------------------------------------------ failures
 w4a4_status w4a4_selftest_wait_timeout(const void* X, const void* L1, int M, int K, int rank, void* T,
                                        unsigned int timeout_us, w4a4_stream_t stream) {

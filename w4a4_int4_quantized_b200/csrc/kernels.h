@@ -81,6 +81,9 @@ struct RowQuantArgs {
 };
 // dtype: 0 bf16, 1 fp16, 2 fp32
 cudaError_t launch_row_quantize(const RowQuantArgs& a, bool silu, int dtype, cudaStream_t st);
+// Host-only view of how it is launched (no CUDA call): {form, chunks of 8 per
+// thread, threads per row, rows per block, stages of a ring}.
+void plan_row_quantize(bool silu, bool second, bool aligned, int dtype, int M, int K, int sms, int out[5]);
 
 // The int8 product for any sizes (csrc/matmul8.cu).  Strides count elements.
 struct Matmul8Args {

@@ -890,35 +890,33 @@ cudaError_t launch_rows(Kernel kern, int64_t grid, int threads, size_t smem, cud
 
 int threads_per_row(int chunks, int vpt) { return ((chunks + vpt - 1) / vpt + 31) / 32 * 32; }
 
-// Rows of one warp, four to a block.
-template <class T, int OP, RowLoads LOADS>
-cudaError_t launch_warp_rows(const RowQuantArgs& a, int vpt, cudaStream_t st) {
-  const int64_t blocks = ((int64_t)a.M + 3) / 4;
-  if (vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 128, LOADS>, blocks, 128, 0, st, a, 32);
-  if (vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 128, LOADS>, blocks, 128, 0, st, a, 32);
-  return launch_rows(row_quantize_kernel<T, OP, 4, 128, LOADS>, blocks, 128, 0, st, a, 32);
-}
-template <class T, int OP, RowLoads LOADS>
-cudaError_t launch_block_rows(const RowQuantArgs& a, int vpt, int tpr, cudaStream_t st) {
-  if (vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 1024, LOADS>, a.M, tpr, 0, st, a, tpr);
-  if (vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 1024, LOADS>, a.M, tpr, 0, st, a, tpr);
-  return launch_rows(row_quantize_kernel<T, OP, 4, 1024, LOADS>, a.M, tpr, 0, st, a, tpr);
-}
+// What a launch is chosen by.
+struct RowShape {
+  int M, K, op;
+  size_t es;         // bytes of an element
+  bool second;       // a residual, or up
+  bool vec;          // rows and weights 16-byte aligned, K a multiple of 8
+};
+struct RowPlan {
+  bool ring;
+  int form;          // RowLayout of a ring, RowLoads of the direct kernel
+  int vpt, tpr, rpb; // chunks per thread, threads per row, rows (or rings) per block
+  int stages, per_sm;
+};
 
 // Chunks per thread of the direct kernel: one, the shortest chain, where there are
 // at most two rows per SM or every row is resident at once, else two (norm of 600 x
 // 768 bf16 2.7 us with one, 2.9 with two; off the alignment 3.3 and 4.4; 600 x 4096
 // 7.5 and 5.6; 900 x 5120 gated 6.8 with two, 7.5 with four), four where one warp then
 // has a row (2000 x 768 4.5 us, with two 4.9) or 1024 threads cannot hold it in two.
-template <class T, int OP>
-cudaError_t launch_direct(const RowQuantArgs& a, bool vec, int sms, cudaStream_t st) {
-  const int chunks = (a.K + 7) / 8;
-  int vpt = a.M <= 2 * sms || (int64_t)a.M * threads_per_row(chunks, 1) <= (int64_t)1024 * sms ? 1 : vec && chunks <= 128 ? 4 : 2;
+RowPlan plan_direct(const RowShape& r, int sms) {
+  const int chunks = (r.K + 7) / 8;
+  int vpt = r.M <= 2 * sms || (int64_t)r.M * threads_per_row(chunks, 1) <= (int64_t)1024 * sms ? 1 : r.vec && chunks <= 128 ? 4 : 2;
   while (vpt < 4 && (chunks + vpt - 1) / vpt > 1024) vpt *= 2;
   while (vpt > 1 && chunks <= 32 * (vpt / 2)) vpt /= 2;
   const int tpr = threads_per_row(chunks, vpt);
-  if (tpr == 32) return vec ? launch_warp_rows<T, OP, kAligned16>(a, vpt, st) : launch_warp_rows<T, OP, kElements>(a, vpt, st);
-  return vec ? launch_block_rows<T, OP, kAligned16>(a, vpt, tpr, st) : launch_block_rows<T, OP, kWindows>(a, vpt, tpr, st);
+  const int form = r.vec ? kAligned16 : tpr == 32 ? kElements : kWindows;
+  return RowPlan{false, form, vpt, tpr, tpr == 32 ? 4 : 1, 0, 0};
 }
 
 // An SM's shared memory for rings: 228 KB less 2 KB for each block (the runtime's
@@ -926,16 +924,12 @@ cudaError_t launch_direct(const RowQuantArgs& a, bool vec, int sms, cudaStream_t
 constexpr int kSmemSm = 228 * 1024, kSmemBlock = 2 * 1024;
 constexpr int kRingMax = 224 * 1024;
 
-struct RingPlan {
-  int vpt, tpr, rpb, stages, per_sm;
-};
-
 // Threads per row, rings and their depth for rows of `stage` bytes.  Four chunks
 // per thread (its share of the two reductions is some 120 instructions), fewer
 // where the rings that fit an SM's memory would then leave it under 512 threads
 // (norm of 8192 x 5120 fp32 96 us with 320 threads, 91 with 640) or where more than 384
 // threads hold four each in 64 registers (4096 x 16384 bf16 111 us, with two 81).
-bool plan_ring(int K, size_t stage, RingPlan& pl) {
+bool plan_ring(int K, size_t stage, RowPlan& pl) {
   const int chunks = (K + 7) / 8;
   int most = 0;
   for (int vpt = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4; vpt >= 1; vpt /= 2) {
@@ -949,15 +943,51 @@ bool plan_ring(int K, size_t stage, RingPlan& pl) {
     if (per_sm * tpr * rpb > most) {
       most = per_sm * tpr * rpb;
       const size_t room = std::min<size_t>(kSmemSm / per_sm - kSmemBlock, kRingMax);
-      pl = RingPlan{vpt, tpr, rpb, (int)std::min<size_t>(kRingStages, room / (stage * rpb)), per_sm};
+      pl = RowPlan{true, 0, vpt, tpr, rpb, (int)std::min<size_t>(kRingStages, room / (stage * rpb)), per_sm};
     }
     if (most >= 512) break;
   }
   return most > 0;
 }
 
+size_t stage_bytes(const RowShape& r) { return slot_bytes((uint32_t)(r.K * r.es), !r.vec) * (r.second ? 2 : 1); }
+
+// The ring pays where rows are long or many; us direct, ring.  Aligned: norm of 1200
+// x 4096 bf16 9.4, 11.1, of 3000 x 4096 19.2, 20.1, of 4608 x 4096 31, 27, of 2000 x 8192
+// 29.6, 26.0; SiLU of 2000 x 5120 12.7, 15.1, of 600 x 14336 15.7, 12.4.  Off the
+// alignment, where the stored sum costs the ring more registers than it saves:
+// norm of 1200 x 8195 28, 35, of 8192 x 4099 80, 95, of 13340 x 5222 168, 163, of 1623 x
+// 14470 69, 55, without a residual of 16384 x 1030 fp32 36, 48, of 16384 x 5003 124, 101;
+// SiLU, which stores none, of 1021 x 5461 fp32 18.0, 13.2, of 1500 x 6001
+// 17.9, 16.5.  At most two rows per SM go direct; rows under 16 bytes have no granule
+// of their own to copy.
+RowPlan plan_rows(const RowShape& r, int sms) {
+  const size_t slot = slot_bytes((uint32_t)(r.K * r.es), !r.vec), stage = stage_bytes(r);
+  const bool much = !r.vec && r.op == 0 ? slot >= 24u * 1024u || (size_t)r.M * slot >= (size_t)80 << 20
+                                        : stage >= 24u * 1024u || (size_t)r.M * stage >= (size_t)(r.vec ? 64 : 32) << 20;
+  RowPlan pl;
+  if (r.M <= 2 * sms || !much || r.K * r.es < 16 || !plan_ring(r.K, stage, pl)) return plan_direct(r, sms);
+  pl.form = !r.vec ? kShifted : r.K == 8 * pl.vpt * pl.tpr ? kWhole : kAligned;
+  return pl;
+}
+
+// Rows of one warp, four to a block.
+template <class T, int OP, RowLoads LOADS>
+cudaError_t launch_warp_rows(const RowQuantArgs& a, const RowPlan& pl, cudaStream_t st) {
+  const int64_t blocks = ((int64_t)a.M + 3) / 4;
+  if (pl.vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 128, LOADS>, blocks, 128, 0, st, a, 32);
+  if (pl.vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 128, LOADS>, blocks, 128, 0, st, a, 32);
+  return launch_rows(row_quantize_kernel<T, OP, 4, 128, LOADS>, blocks, 128, 0, st, a, 32);
+}
+template <class T, int OP, RowLoads LOADS>
+cudaError_t launch_block_rows(const RowQuantArgs& a, const RowPlan& pl, cudaStream_t st) {
+  if (pl.vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 1024, LOADS>, a.M, pl.tpr, 0, st, a, pl.tpr);
+  if (pl.vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 1024, LOADS>, a.M, pl.tpr, 0, st, a, pl.tpr);
+  return launch_rows(row_quantize_kernel<T, OP, 4, 1024, LOADS>, a.M, pl.tpr, 0, st, a, pl.tpr);
+}
+
 template <class T, int OP, int VPT, int MAXT, RowLayout LAY>
-cudaError_t launch_ring_t(const RowQuantArgs& a, const RingPlan& pl, size_t stage, int sms, int dev, cudaStream_t st) {
+cudaError_t launch_ring_t(const RowQuantArgs& a, const RowPlan& pl, size_t stage, int sms, int dev, cudaStream_t st) {
   auto kern = row_ring_kernel<T, OP, VPT, MAXT, LAY>;
   static DeviceFlags configured;
   cudaError_t e;
@@ -973,10 +1003,9 @@ cudaError_t launch_ring_t(const RowQuantArgs& a, const RingPlan& pl, size_t stag
 }
 
 template <class T, int OP, int VPT, int MAXT>
-cudaError_t launch_ring(const RowQuantArgs& a, const RingPlan& pl, bool vec, size_t stage, int sms, int dev,
-                        cudaStream_t st) {
-  if (!vec) return launch_ring_t<T, OP, VPT, MAXT, kShifted>(a, pl, stage, sms, dev, st);
-  if (a.K == 8 * VPT * pl.tpr) return launch_ring_t<T, OP, VPT, MAXT, kWhole>(a, pl, stage, sms, dev, st);
+cudaError_t launch_ring(const RowQuantArgs& a, const RowPlan& pl, size_t stage, int sms, int dev, cudaStream_t st) {
+  if (pl.form == kShifted) return launch_ring_t<T, OP, VPT, MAXT, kShifted>(a, pl, stage, sms, dev, st);
+  if (pl.form == kWhole) return launch_ring_t<T, OP, VPT, MAXT, kWhole>(a, pl, stage, sms, dev, st);
   return launch_ring_t<T, OP, VPT, MAXT, kAligned>(a, pl, stage, sms, dev, st);
 }
 
@@ -991,26 +1020,19 @@ cudaError_t launch_op(const RowQuantArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
-  // The ring pays where rows are long or many; us direct, ring.  Aligned: norm of 1200
-  // x 4096 bf16 9.4, 11.1, of 3000 x 4096 19.2, 20.1, of 4608 x 4096 31, 27, of 2000 x 8192
-  // 29.6, 26.0; SiLU of 2000 x 5120 12.7, 15.1, of 600 x 14336 15.7, 12.4.  Off the
-  // alignment, where the stored sum costs the ring more registers than it saves:
-  // norm of 1200 x 8195 28, 35, of 8192 x 4099 80, 95, of 13340 x 5222 168, 163, of 1623 x
-  // 14470 69, 55, without a residual of 16384 x 1030 fp32 36, 48, of 16384 x 5003 124, 101;
-  // SiLU, which stores none, of 1021 x 5461 fp32 18.0, 13.2, of 1500 x 6001
-  // 17.9, 16.5.  At most two rows per SM go direct; rows under 16 bytes have no granule
-  // of their own to copy.
-  RingPlan pl;
-  const size_t slot = slot_bytes((uint32_t)(a.K * es), !vec), stage = slot * (a.B ? 2 : 1);
-  const bool much = !vec && OP == 0 ? slot >= 24u * 1024u || (size_t)a.M * slot >= (size_t)80 << 20
-                                    : stage >= 24u * 1024u || (size_t)a.M * stage >= (size_t)(vec ? 64 : 32) << 20;
-  if (a.M <= 2 * sms || !much || a.K * es < 16 || !plan_ring(a.K, stage, pl)) return launch_direct<T, OP>(a, vec, sms, st);
-  if (pl.vpt == 1 && pl.tpr <= 384) return launch_ring<T, OP, 1, 384>(a, pl, vec, stage, sms, dev, st);
-  if (pl.vpt == 1) return launch_ring<T, OP, 1, 1024>(a, pl, vec, stage, sms, dev, st);
-  if (pl.vpt == 2 && pl.tpr <= 384) return launch_ring<T, OP, 2, 384>(a, pl, vec, stage, sms, dev, st);
-  if (pl.vpt == 2) return launch_ring<T, OP, 2, 1024>(a, pl, vec, stage, sms, dev, st);
-  if (pl.tpr <= 384) return launch_ring<T, OP, 4, 384>(a, pl, vec, stage, sms, dev, st);
-  return launch_ring<T, OP, 4, 1024>(a, pl, vec, stage, sms, dev, st);
+  const RowShape shape{a.M, a.K, OP, es, a.B != nullptr, vec};
+  const RowPlan pl = plan_rows(shape, sms);
+  if (!pl.ring) {
+    if (pl.tpr == 32) return vec ? launch_warp_rows<T, OP, kAligned16>(a, pl, st) : launch_warp_rows<T, OP, kElements>(a, pl, st);
+    return vec ? launch_block_rows<T, OP, kAligned16>(a, pl, st) : launch_block_rows<T, OP, kWindows>(a, pl, st);
+  }
+  const size_t stage = stage_bytes(shape);
+  if (pl.vpt == 1 && pl.tpr <= 384) return launch_ring<T, OP, 1, 384>(a, pl, stage, sms, dev, st);
+  if (pl.vpt == 1) return launch_ring<T, OP, 1, 1024>(a, pl, stage, sms, dev, st);
+  if (pl.vpt == 2 && pl.tpr <= 384) return launch_ring<T, OP, 2, 384>(a, pl, stage, sms, dev, st);
+  if (pl.vpt == 2) return launch_ring<T, OP, 2, 1024>(a, pl, stage, sms, dev, st);
+  if (pl.tpr <= 384) return launch_ring<T, OP, 4, 384>(a, pl, stage, sms, dev, st);
+  return launch_ring<T, OP, 4, 1024>(a, pl, stage, sms, dev, st);
 }
 
 template <class T>
@@ -1019,6 +1041,15 @@ cudaError_t launch_type(const RowQuantArgs& a, bool silu, cudaStream_t st) {
 }
 
 }  // namespace
+
+void plan_row_quantize(bool silu, bool second, bool aligned, int dtype, int M, int K, int sms, int out[5]) {
+  const RowPlan pl = plan_rows(RowShape{M, K, silu ? 1 : 0, dtype == 2 ? 4u : 2u, second, aligned && K % 8 == 0}, sms);
+  out[0] = pl.ring ? 3 + pl.form : pl.form;
+  out[1] = pl.vpt;
+  out[2] = pl.tpr;
+  out[3] = pl.rpb;
+  out[4] = pl.stages;
+}
 
 cudaError_t launch_row_quantize(const RowQuantArgs& a, bool silu, int dtype, cudaStream_t st) {
   if (dtype == 0) return launch_type<Bf16>(a, silu, st);
