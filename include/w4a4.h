@@ -395,6 +395,16 @@ w4a4_status w4a4_plan_gemm_split(int M, int N, int K, int rank, int sms, int clu
  * The pages have no counterpart. */
 w4a4_status w8a8_plan_rows(int silu, int second, int aligned, int M, int K, w4a4_dtype dtype, int sms, int* plan);
 
+/* The same for w8a8_matmul.  clusters: how many clusters of a kind fit the device
+ * at once, clusters[0..2] of 2, 4 and 8 CTAs that share an SM with one other,
+ * clusters[3..5] of 4, 6 and 8 CTAs with an SM each; NULL asks the current device
+ * (sms is then its own too), else no CUDA call is made.  Writes plan[3]:
+ *   plan[0]  0 the few-token kernel, 1 streamed weights, 2 pair tiles;
+ *   plan[1]  0 and 1: tokens per tile, 2: columns per tile;
+ *   plan[2]  slices of K. */
+w4a4_status w8a8_plan_matmul(int M, int N, int K, int64_t ldx, int64_t ldw, w4a4_dtype dtype, int sms,
+                             const int* clusters, int* plan);
+
 /* ---------------------------------------------------------------- failures */
 /* Kernels never trap: a wait on another part of the kernel that runs past its
  * time limit (2 s) records a code in a per-device error word and lets the

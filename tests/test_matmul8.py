@@ -411,3 +411,74 @@ def test_other_host_threads_run_while_a_call_waits(tmp_path):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", _LOCK, str(lib)], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "ran" in r.stdout, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ every form of the product
+EVERY_FORM = [
+    # kernel, tokens or columns per tile, slices of K, M, N, K: what w8a8_plan_matmul gives on 148 SMs
+    (0, 8, 1, 1, 48, 64), (0, 8, 1, 1, 65, 71), (0, 16, 1, 9, 48, 64), (0, 16, 1, 9, 67, 75), (0, 32, 1, 17, 48, 64),
+    (0, 32, 1, 17, 69, 65),
+    (1, 16, 1, 10, 4824, 64), (1, 16, 1, 13, 4939, 67), (1, 16, 2, 15, 5784, 960), (1, 16, 2, 11, 5713, 933),
+    (1, 16, 4, 11, 4824, 1024), (1, 16, 4, 15, 5141, 909), (1, 16, 8, 10, 48, 9344), (1, 16, 8, 13, 65, 8293),
+    (1, 32, 1, 18, 4776, 64), (1, 32, 1, 23, 5507, 67), (1, 32, 2, 23, 4776, 960), (1, 32, 2, 23, 4777, 905),
+    (1, 32, 4, 30, 4896, 1408), (1, 32, 4, 19, 5143, 1381), (1, 32, 8, 23, 48, 4160), (1, 32, 8, 23, 65, 4147),
+    (1, 64, 1, 36, 48, 64), (1, 64, 1, 35, 69, 71), (1, 64, 2, 39, 48, 832), (1, 64, 2, 35, 81, 673),
+    (1, 64, 4, 35, 48, 960), (1, 64, 4, 35, 65, 925), (1, 64, 8, 36, 48, 1984), (1, 64, 8, 45, 67, 1931),
+    (1, 128, 1, 77, 18960, 64), (1, 128, 1, 69, 19327, 69), (1, 128, 2, 66, 9600, 3008), (1, 128, 2, 67, 10505, 2695),
+    (1, 128, 4, 75, 4512, 6080), (1, 128, 4, 69, 5655, 4503), (1, 128, 8, 72, 2400, 8384), (1, 128, 8, 1057, 149, 11321),
+    (2, 128, 1, 194, 19632, 64), (2, 128, 1, 199, 19573, 69), (2, 128, 2, 2188, 264, 3136), (2, 128, 2, 2147, 273, 3089),
+    (2, 128, 3, 1547, 264, 2240), (2, 128, 3, 2763, 131, 2243), (2, 128, 4, 1547, 144, 4160), (2, 128, 4, 1569, 131, 4119),
+    (2, 256, 1, 258, 16296, 64), (2, 256, 1, 265, 15177, 71), (2, 256, 2, 332, 3312, 2752), (2, 256, 2, 545, 2057, 2763),
+    (2, 256, 3, 72, 5112, 3648), (2, 256, 3, 2103, 265, 3405), (2, 256, 4, 784, 648, 2880), (2, 256, 4, 2925, 133, 3351),
+]
+
+
+def test_every_form_has_its_cases(lib):
+    """The cases take the forms that they are listed under, an even and a ragged one each, and no size takes
+    a form that is not among them."""
+    rng = np.random.default_rng(8)
+    kinds = {(0, w, 1) for w in (8, 16, 32)} | {(1, w, s) for w in (16, 32, 64, 128) for s in (1, 2, 4, 8)} | \
+        {(2, w, s) for w in (128, 256) for s in (1, 2, 3, 4)}
+    assert {(*c[:3], c[5] % 2) for c in EVERY_FORM} == {(*k, odd) for k in kinds for odd in (0, 1)}
+    for *form, M, N, K in EVERY_FORM:
+        for dtype in ("bf16", "fp16", "fp32"):
+            assert w4.w8a8_plan_matmul(M, N, K, dtype) == tuple(form), (M, N, K, dtype)
+    for _ in range(5000):
+        M, N, K = np.exp(rng.uniform(0, np.log([9000, 30000, 131071]))).astype(int)
+        assert w4.w8a8_plan_matmul(int(M), int(N), int(K), "fp32") in kinds
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("kernel,width,split,M,N,K", EVERY_FORM)
+def test_every_form(kernel, width, split, M, N, K, dtype):
+    """With and without a bias, rows of Y on and off the alignment of a wide store."""
+    import torch
+    for bias, pad, offset in ((True, -N % 8, 0), (False, 3, 1), (True, 2, 2)):
+        Xq, sx, Wq, sw, v = _case(M, N, K, M + N + K + offset, dtype, bias)
+        ldy = N + pad
+        buf = torch.full(((M + 1) * ldy + offset,), 5.0, dtype=_dt(dtype), device="cuda")
+        Y = buf[offset:].as_strided((M, N), (ldy, 1))
+        w4.w8a8_matmul(Xq, sx, Wq, sw, 64, v, Y=Y)
+        torch.cuda.synchronize()
+        check_product(Y, Xq, sx, Wq, sw, 64, v)
+        Y.fill_(5.0)
+        assert (buf == 5.0).all()                     # nothing between the rows, before or behind them
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(256, 4096, 12288), (512, 4096, 4096), (256, 2048, 16384), (509, 4001, 4111)])
+def test_split_products_of_ordinary_size(M, N, K):
+    test_product(M, N, K, 128, "bf16")
+
+
+def test_plan_refusals(lib):
+    import ctypes
+    f = lib.w8a8_plan_matmul
+    cl, out = (ctypes.c_int * 6)(148, 71, 33, 33, 22, 15), (ctypes.c_int * 3)()
+    assert f(4, 64, 64, 64, 64, 0, 148, cl, out) == OK
+    assert f(4, 64, 64, 64, 64, 0, 148, cl, None) == INVALID and f(4, 64, 64, 64, 64, 3, 148, cl, out) == INVALID
+    for bad in ((0, 64, 64, 64, 64), (4, 0, 64, 64, 64), (4, 64, 0, 64, 64), (4, 64, 131072, 131072, 131072),
+                (4, 64, 64, 48, 64), (4, 64, 64, 64, 72)):
+        assert f(*bad, 0, 148, cl, out) == SHAPE, bad
+    assert f(4, 64, 64, 64, 64, 0, 1, cl, out) == SHAPE

@@ -28,7 +28,7 @@ __all__ = [
     "w8a8_workspace_bytes", "w4a8_quantize_weights", "w4a8_gemm", "w4a8_linear", "w4a8_workspace_bytes",
     "w4a4_lora_merge", "w4a4_gemm_gelu", "w4a4_linear_gelu", "w4a4_mlp", "w4a4_mlp_workspace_bytes",
     "w4a4_bake_lora_sr", "w4a4_get_device_error", "w4a4_selftest_wait_timeout", "w4a4_plan_rotate_quantize",
-    "w4a4_plan_gemm_split", "w8a8_plan_rows",
+    "w4a4_plan_gemm_split", "w8a8_plan_rows", "w8a8_plan_matmul",
     "w8a8_add_rmsnorm_quantize", "w8a8_silu_mul_quantize", "w8a8_matmul",
     "DEVERR_WAIT_OPERANDS", "DEVERR_WAIT_SLOT", "DEVERR_WAIT_ACCUM", "DEVERR_WAIT_DRAIN",
 ]
@@ -98,6 +98,7 @@ def load_library():
         "w4a4_selftest_wait_timeout": ([P, P, I, I, I, P, ctypes.c_uint, P], S),
         "w4a4_plan_rotate_quantize": ([I, I, I, I, I, I, ctypes.POINTER(ctypes.c_int)], S),
         "w4a4_plan_gemm_split": ([I, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_int)], S),
+        "w8a8_plan_matmul": ([I, I, I, L, L, I, I, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)], S),
         "w8a8_plan_rows": ([I, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_int)], S),
     }
     for name, (args, res) in sig.items():
@@ -569,4 +570,17 @@ def w8a8_plan_rows(silu, M, K, dtype="bf16", residual=True, aligned=True, sms=14
     out = (ctypes.c_int * 5)()
     _check("w8a8_plan_rows", load_library().w8a8_plan_rows(
         1 if silu else 0, 1 if residual else 0, 1 if aligned else 0, M, K, ("bf16", "fp16", "fp32").index(dtype), sms, out))
+    return tuple(out)
+
+
+def w8a8_plan_matmul(M, N, K, dtype="bf16", ldx=None, ldw=None, sms=148, clusters=(148, 71, 33, 33, 22, 15)):
+    """The form w8a8_matmul takes: (kernel, tokens or columns per tile, slices of
+    K), as in include/w4a4.h.  Host only for a device with `sms` SMs on which the
+    given numbers of clusters fit; clusters=None asks the current device.  Strides
+    default to K rounded up to 16."""
+    out = (ctypes.c_int * 3)()
+    row = (K + 15) // 16 * 16
+    _check("w8a8_plan_matmul", load_library().w8a8_plan_matmul(
+        M, N, K, ldx or row, ldw or row, ("bf16", "fp16", "fp32").index(dtype), sms,
+        None if clusters is None else (ctypes.c_int * 6)(*clusters), out))
     return tuple(out)

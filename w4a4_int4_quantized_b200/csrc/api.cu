@@ -487,6 +487,28 @@ w4a4_status w8a8_plan_rows(int silu, int second, int aligned, int M, int K, w4a4
   return W4A4_OK;
 }
 
+w4a4_status w8a8_plan_matmul(int M, int N, int K, int64_t ldx, int64_t ldw, w4a4_dtype dtype, int sms,
+                             const int* clusters, int* plan) {
+  if (!plan || !dtype_ok(dtype)) return W4A4_ERR_INVALID_ARG;
+  if (M < 1 || N < 1 || K < 1 || K > 131071 || !code_rows_ok(M, ldx, K) || !code_rows_ok(N, ldw, K) ||
+      (clusters && sms < 2))
+    return W4A4_ERR_UNSUPPORTED_SHAPE;
+  int dev = 0;
+  if (!clusters) {
+    const w4a4_status s = check_device();
+    if (s != W4A4_OK) return s;
+    if (cudaGetDevice(&dev) != cudaSuccess || device_sm_count(dev, &sms) != cudaSuccess) return W4A4_ERR_CUDA;
+  }
+  Matmul8Args a{};
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.lda = ldx;
+  a.ldb = ldw;
+  plan_matmul8(a, (int)dtype, sms, dev, clusters, plan);
+  return W4A4_OK;
+}
+
 // ------------------------------------------------------------------ failures
 w4a4_status w4a4_selftest_wait_timeout(const void* X, const void* L1, int M, int K, int rank, void* T,
                                        unsigned int timeout_us, w4a4_stream_t stream) {

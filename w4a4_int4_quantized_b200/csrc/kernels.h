@@ -100,5 +100,9 @@ struct Matmul8Args {
 };
 // dtype of Y and bias: 0 bf16, 1 fp16, 2 fp32
 cudaError_t launch_matmul8(const Matmul8Args& a, int dtype, cudaStream_t st);
+// The form that it takes: {kernel, tokens or columns per tile, slices of K}, from
+// the sizes and strides of a; clusters: residency of six kinds of clusters, or null
+// for device dev's own.
+void plan_matmul8(const Matmul8Args& a, int dtype, int sms, int dev, const int* clusters, int out[3]);
 
 }  // namespace w4a4

@@ -1083,12 +1083,24 @@ int resident_streams(int split, int dev) {
 }
 
 // A form of the product and its modelled time in us.
+enum FormKernel { kFew, kStream, kTile };
 struct Form {
-  int nt;        // streamed: tokens per tile; 0: pair tiles
-  int bn;        // pair tiles: their width
+  FormKernel kernel;
+  int width;     // few tokens and streamed: tokens per tile; pair tiles: their columns
   int split;
   float cost;
 };
+
+// How many clusters are resident at once: `given` for streams in clusters of 2, 4
+// and 8 CTAs and pair tiles of 2, 3 and 4 pairs, or, null, what this device says.
+template <int NT, class O>
+int streams_at_once(int split, int dev, const int* given) {
+  return given ? given[split == 2 ? 0 : split == 4 ? 1 : 2] : resident_streams<NT, O>(split, dev);
+}
+template <int BN, class O>
+int tiles_at_once(int split, int dev, const int* given) {
+  return given ? given[1 + split] : resident_tiles<BN, O>(split, dev);
+}
 
 // What every form moves at least, in us.
 template <class O>
@@ -1102,7 +1114,7 @@ float memory_time(const Matmul8Args& a) {
 // a further wave 3 to 5.5 besides its k-blocks of 0.36 or 0.42; a split 0.8 for its
 // cluster barriers and its sums' way between SMs at 3.5 MB per us.
 template <int NT, class O>
-void consider_streamed(const Matmul8Args& a, int sms, int dev, Form& best) {
+void consider_streamed(const Matmul8Args& a, int sms, int dev, const int* given, Form& best) {
   constexpr float base = NT <= 32 ? 2.8f : NT == 64 ? 3.0f : 4.0f, wave = NT <= 32 ? 3.0f : NT == 64 ? 4.0f : 5.5f;
   const float lines = NT == 64 && (a.lda | a.ldb) % BK != 0 ? 1.15f : 1.0f;
   const float kb = lines * (NT <= 64 ? 0.26f : 0.37f), wave_kb = lines * (NT <= 64 ? 0.36f : 0.42f);
@@ -1110,13 +1122,13 @@ void consider_streamed(const Matmul8Args& a, int sms, int dev, Form& best) {
   const int nk = (a.K + BK - 1) / BK;
   if (tiles > 0x7FFFFFFF / 8) return;
   for (int s = 1; s <= 8; s *= 2) {
-    if (s > 1 && (nk < 2 * s || tiles * s > 2 * (int64_t)sms || tiles > resident_streams<NT, O>(s, dev))) break;
+    if (s > 1 && (nk < 2 * s || tiles * s > 2 * (int64_t)sms || tiles > streams_at_once<NT, O>(s, dev, given))) break;
     const int64_t ctas = tiles * s, waves = (ctas + 2 * sms - 1) / (2 * sms);
     const float per = (float)((nk + s - 1) / s);
     const float work = per * kb * (ctas > sms ? 1.4f : 1.0f) + (float)(waves - 1) * (wave + per * wave_kb);
     float cost = std::max(memory_time<O>(a), work) + base;
     if (s > 1) cost += 0.8f + (float)(ctas * NT * kStreamRows * 4 / s * (s - 1)) * (1.0f / 3.5e6f);
-    if (cost < best.cost) best = Form{NT, 0, s, cost};
+    if (cost < best.cost) best = Form{kStream, NT, s, cost};
   }
 }
 
@@ -1126,18 +1138,18 @@ void consider_streamed(const Matmul8Args& a, int sms, int dev, Form& best) {
 // cost a second round (256 x 4096 x 12288 in quarters 34 us, in thirds 19.4), so they
 // are not considered.
 template <int BN, class O>
-void consider_tiled(const Matmul8Args& a, int sms, int dev, Form& best) {
+void consider_tiled(const Matmul8Args& a, int sms, int dev, const int* given, Form& best) {
   constexpr float kb = BN == 256 ? 0.30f : 0.28f, base = BN == 256 ? 5.8f : 4.7f, epilogue = BN == 256 ? 3.1f : 1.75f;
   const int64_t tiles = (((int64_t)a.M + 2 * BM - 1) / (2 * BM)) * (((int64_t)a.N + BN - 1) / BN);
   const int nk = (a.K + BK - 1) / BK, pairs = sms / 2;
   for (int s = 1; s <= 4; ++s) {
     if (s > 1 && (nk < 2 * s || tiles * s > pairs)) break;
-    if (s > 1 && tiles > resident_tiles<BN, O>(s, dev)) continue;
+    if (s > 1 && tiles > tiles_at_once<BN, O>(s, dev, given)) continue;
     const int64_t rounds = s > 1 ? 1 : (tiles + pairs - 1) / pairs;
     const float per = (float)((nk + s - 1) / s) * kb;
     const float work = per + (float)(rounds - 1) * std::max(per, epilogue);
     const float cost = std::max(memory_time<O>(a), work) + base + (s > 1 ? 1.75f : 0.0f);
-    if (cost < best.cost) best = Form{0, BN, s, cost};
+    if (cost < best.cost) best = Form{kTile, BN, s, cost};
   }
 }
 
@@ -1149,11 +1161,7 @@ void consider_tiled(const Matmul8Args& a, int sms, int dev, Form& best) {
 // 12288 pair tiles in halves 22.5 (streamed 27.5); 1000, 14336 x 4096 pair tiles 51
 // (65); 7404, 18199 x 27 pair tiles 114 (180).
 template <class O>
-cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
+Form choose_form(const Matmul8Args& a, int sms, int dev, const int* given) {
   // Few tokens (us against the best streamed form).  Up to 8, with 52 MB of weights and
   // 8192 codes of k, or 16 MB and 16384, at most; 8 tokens: 4096 x 4096 5.1 (6.6), 12288 x
   // 4096 10.4 (12.4), 14336 x 4096 13.4 (13.2), 6144 x 8192 9.3 (12.9), 8192 x 8192 16.8
@@ -1162,28 +1170,53 @@ cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
   // 8.8 (12.1), 14336 x 1024 6.4 (6.1).  Up to 32, with 4096 codes besides: 1024 x 1024 2.6
   // (4.3), 4096 x 4096 6.7 (6.9), 2048 x 8192 9.5 (7.5).
   const bool resident = a.N <= 2 * sms * kFewRows;
-  if (a.M <= 8 && a.K <= 16384 && (int64_t)a.N * a.K <= (int64_t)(a.K <= 8192 ? 52 : 16) << 20) return launch_few<1, O>(a, sms, st);
-  if (a.M <= 16 && a.K <= 8192 && resident) return launch_few<2, O>(a, sms, st);
-  if (a.M <= 32 && a.K <= 4096 && resident) return launch_few<4, O>(a, sms, st);
-  Form f{0, 0, 0, 1e30f};
-  if (a.M <= 16) consider_streamed<16, O>(a, sms, dev, f);
-  else if (a.M <= 32) consider_streamed<32, O>(a, sms, dev, f);
-  else consider_streamed<64, O>(a, sms, dev, f);
-  if (a.M > 64) consider_streamed<128, O>(a, sms, dev, f);
-  consider_tiled<256, O>(a, sms, dev, f);
-  consider_tiled<128, O>(a, sms, dev, f);
-  switch (f.nt) {
-    case 16: return launch_stream<16, O>(a, f.split, dev, st);
-    case 32: return launch_stream<32, O>(a, f.split, dev, st);
-    case 64: return launch_stream<64, O>(a, f.split, dev, st);
-    case 128: return launch_stream<128, O>(a, f.split, dev, st);
+  if (a.M <= 8 && a.K <= 16384 && (int64_t)a.N * a.K <= (int64_t)(a.K <= 8192 ? 52 : 16) << 20) return Form{kFew, 8, 1, 0.0f};
+  if (a.M <= 16 && a.K <= 8192 && resident) return Form{kFew, 16, 1, 0.0f};
+  if (a.M <= 32 && a.K <= 4096 && resident) return Form{kFew, 32, 1, 0.0f};
+  Form f{kTile, 0, 0, 1e30f};
+  if (a.M <= 16) consider_streamed<16, O>(a, sms, dev, given, f);
+  else if (a.M <= 32) consider_streamed<32, O>(a, sms, dev, given, f);
+  else consider_streamed<64, O>(a, sms, dev, given, f);
+  if (a.M > 64) consider_streamed<128, O>(a, sms, dev, given, f);
+  consider_tiled<256, O>(a, sms, dev, given, f);
+  consider_tiled<128, O>(a, sms, dev, given, f);
+  return f;
+}
+
+template <class O>
+cudaError_t launch_out(const Matmul8Args& a, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if ((e = device_sm_count(dev, &sms)) != cudaSuccess) return e;
+  const Form f = choose_form<O>(a, sms, dev, nullptr);
+  if (f.kernel == kFew) {
+    if (f.width == 8) return launch_few<1, O>(a, sms, st);
+    return f.width == 16 ? launch_few<2, O>(a, sms, st) : launch_few<4, O>(a, sms, st);
   }
-  const TilePlan pl{(int)(((int64_t)a.M + 2 * BM - 1) / (2 * BM)), (int)(((int64_t)a.N + f.bn - 1) / f.bn), f.split};
-  if (f.bn == 128) return f.split > 1 ? launch_tile<128, O, true>(a, pl, sms, dev, st) : launch_tile<128, O, false>(a, pl, sms, dev, st);
+  if (f.kernel == kStream) {
+    switch (f.width) {
+      case 16: return launch_stream<16, O>(a, f.split, dev, st);
+      case 32: return launch_stream<32, O>(a, f.split, dev, st);
+      case 64: return launch_stream<64, O>(a, f.split, dev, st);
+      default: return launch_stream<128, O>(a, f.split, dev, st);
+    }
+  }
+  const TilePlan pl{(int)(((int64_t)a.M + 2 * BM - 1) / (2 * BM)), (int)(((int64_t)a.N + f.width - 1) / f.width), f.split};
+  if (f.width == 128) return f.split > 1 ? launch_tile<128, O, true>(a, pl, sms, dev, st) : launch_tile<128, O, false>(a, pl, sms, dev, st);
   return f.split > 1 ? launch_tile<256, O, true>(a, pl, sms, dev, st) : launch_tile<256, O, false>(a, pl, sms, dev, st);
 }
 
 }  // namespace
+
+void plan_matmul8(const Matmul8Args& a, int dtype, int sms, int dev, const int* clusters, int out[3]) {
+  const Form f = dtype == 0   ? choose_form<OutBf16>(a, sms, dev, clusters)
+                 : dtype == 1 ? choose_form<OutFp16>(a, sms, dev, clusters)
+                              : choose_form<OutFp32>(a, sms, dev, clusters);
+  out[0] = (int)f.kernel;
+  out[1] = f.width;
+  out[2] = f.split;
+}
 
 cudaError_t launch_matmul8(const Matmul8Args& a, int dtype, cudaStream_t st) {
   if (dtype == 0) return launch_out<OutBf16>(a, st);
