@@ -482,3 +482,32 @@ def test_plan_refusals(lib):
                 (4, 64, 64, 48, 64), (4, 64, 64, 64, 72)):
         assert f(*bad, 0, 148, cl, out) == SHAPE, bad
     assert f(4, 64, 64, 64, 64, 0, 1, cl, out) == SHAPE
+
+
+@gpu
+def test_each_refusal_of_the_binding_has_its_status():
+    """One argument at a time is wrong, and the call is refused for it."""
+    import torch
+    Xq, sx, Wq, sw, v = _case(4, 64, 128, 1, "bf16", True)
+    good = dict(Xq=Xq, x_scale=sx, Wq=Wq, w_scale=sw, bias=v)
+    Y = torch.full((5, 80), 3.0, dtype=torch.bfloat16, device="cuda")
+    bad = [(SHAPE, dict(Y=Y[:4, :63])), (SHAPE, dict(Y=Y[:4, :65])), (SHAPE, dict(Y=Y[:3, :64])), (SHAPE, dict(Y=Y[0, :64])),
+           (SHAPE, dict(Y=Y[:4, 0:64:2])), (SHAPE, dict(Y=Y[:1, :64].expand(4, 64))), (INVALID, dict(Y=Y[:4, :64].float())),
+           (INVALID, dict(Y=Y[:4, :64].cpu())), (INVALID, dict(Y=Y[:4, :64], dtype=torch.float16)),
+           (INVALID, dict(bias=None, dtype=torch.float64)), (INVALID, dict(bias=None, Y=Y[:4, :64].double())),
+           (INVALID, dict(bias=v.float())), (INVALID, dict(bias=v.cpu())), (SHAPE, dict(bias=v[:63])),
+           (SHAPE, dict(bias=v[None])), (SHAPE, dict(bias=torch.cat([v, v])[::2])),
+           (SHAPE, dict(x_scale=sx[:3])), (INVALID, dict(x_scale=sx.double())), (SHAPE, dict(w_scale=sw[:8])),
+           (INVALID, dict(w_scale=sw.half())), (SHAPE, dict(Wq=Wq[:, :64])), (INVALID, dict(Wq=Wq.cpu())),
+           (INVALID, dict(Wq=Wq.view(torch.uint8))), (INVALID, dict(Xq=Xq.view(torch.uint8))), (SHAPE, dict(group=3)),
+           (SHAPE, dict(group=-64)), (SHAPE, dict(Wq=torch.zeros(64, 136, dtype=torch.int8, device="cuda")[:, :128])),
+           (MISALIGNED, dict(Xq=torch.zeros(4, 160, dtype=torch.int8, device="cuda")[:, 8:136]))]
+    for status, kw in bad:
+        with pytest.raises(w4.W4A4Error) as e:
+            w4.w8a8_matmul(**{**good, **kw})
+        assert e.value.status == status, (kw.keys(), e.value)
+    with pytest.raises(w4.W4A4Error) as e:
+        w4.w8a8_matmul(Xq.cpu(), sx, Wq, sw)
+    assert e.value.status == 6
+    torch.cuda.synchronize()
+    assert (Y == 3.0).all()

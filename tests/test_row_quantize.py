@@ -579,3 +579,34 @@ def test_a_group_past_32_bits_is_refused(group):
         with pytest.raises(w4.W4A4Error) as e:
             call()
         assert e.value.status == SHAPE
+
+
+@gpu
+def test_each_refusal_of_the_binding_has_its_status():
+    """One argument at a time is wrong, and the call is refused for it."""
+    import torch
+    X = torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")
+    code = torch.zeros((5, 160), dtype=torch.int8, device="cuda")
+    s = torch.zeros(5, device="cuda")
+    common = [(SHAPE, dict(Xq=code[:3, :128])), (SHAPE, dict(Xq=code[:4, :127])), (MISALIGNED, dict(Xq=code[:4, 8:136])),
+              (SHAPE, dict(Xq=torch.zeros((4, 136), dtype=torch.int8, device="cuda")[:, :128])),
+              (INVALID, dict(Xq=code[:4, :128].view(torch.uint8))), (INVALID, dict(Xq=code[:4, :128].cpu())),
+              (SHAPE, dict(x_scale=s)), (INVALID, dict(x_scale=s[:4].double())),
+              (SHAPE, dict(x_scale=torch.zeros(8, device="cuda")[::2])), (SHAPE, dict(group=48)), (SHAPE, dict(group=-64))]
+    norm = [(SHAPE, dict(gamma=X[0, :64])), (INVALID, dict(gamma=X[0].float())), (INVALID, dict(gamma=X[0].cpu())),
+            (SHAPE, dict(residual=X[:3])), (INVALID, dict(residual=X.float())), (SHAPE, dict(H=X[:, :64])),
+            (INVALID, dict(H=X.half())), (SHAPE, dict(H=X[:1].expand(4, 128))), (INVALID, dict(eps=0.0)),
+            (INVALID, dict(eps=float("nan"))), (INVALID, dict(X=X.double())),
+            (SHAPE, dict(X=torch.zeros((128, 4), dtype=torch.bfloat16, device="cuda").t()))]
+    for status, kw in common + norm:
+        with pytest.raises(w4.W4A4Error) as e:
+            w4.w8a8_add_rmsnorm_quantize(**{**dict(X=X, gamma=None, eps=EPS), **kw})
+        assert e.value.status == status, (kw.keys(), e.value)
+    for status, kw in common + [(SHAPE, dict(up=X[:3])), (INVALID, dict(up=X.half())), (INVALID, dict(up=X.cpu())),
+                                (SHAPE, dict(up=torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")[:, ::2])),
+                                (SHAPE, dict(gate=X[:1].expand(4, 128)))]:
+        with pytest.raises(w4.W4A4Error) as e:
+            w4.w8a8_silu_mul_quantize(**{**dict(gate=X, up=X), **kw})
+        assert e.value.status == status, (kw.keys(), e.value)
+    torch.cuda.synchronize()
+    assert not code.any() and not s.any()
