@@ -977,7 +977,8 @@ cudaError_t launch_warp_rows(const RowQuantArgs& a, const RowPlan& pl, cudaStrea
   const int64_t blocks = ((int64_t)a.M + 3) / 4;
   if (pl.vpt == 1) return launch_rows(row_quantize_kernel<T, OP, 1, 128, LOADS>, blocks, 128, 0, st, a, 32);
   if (pl.vpt == 2) return launch_rows(row_quantize_kernel<T, OP, 2, 128, LOADS>, blocks, 128, 0, st, a, 32);
-  return launch_rows(row_quantize_kernel<T, OP, 4, 128, LOADS>, blocks, 128, 0, st, a, 32);
+  if constexpr (LOADS == kAligned16) return launch_rows(row_quantize_kernel<T, OP, 4, 128, LOADS>, blocks, 128, 0, st, a, 32);
+  else return cudaErrorInvalidConfiguration;           // plan_direct: four chunks in one warp only where aligned
 }
 template <class T, int OP, RowLoads LOADS>
 cudaError_t launch_block_rows(const RowQuantArgs& a, const RowPlan& pl, cudaStream_t st) {
@@ -1005,7 +1006,10 @@ cudaError_t launch_ring_t(const RowQuantArgs& a, const RowPlan& pl, size_t stage
 template <class T, int OP, int VPT, int MAXT>
 cudaError_t launch_ring(const RowQuantArgs& a, const RowPlan& pl, size_t stage, int sms, int dev, cudaStream_t st) {
   if (pl.form == kShifted) return launch_ring_t<T, OP, VPT, MAXT, kShifted>(a, pl, stage, sms, dev, st);
-  if (pl.form == kWhole) return launch_ring_t<T, OP, VPT, MAXT, kWhole>(a, pl, stage, sms, dev, st);
+  if (pl.form == kWhole) {
+    if constexpr (T::kWords == 8 && OP == 1 && VPT == 4) return cudaErrorInvalidConfiguration;   // see launch_op
+    else return launch_ring_t<T, OP, VPT, MAXT, kWhole>(a, pl, stage, sms, dev, st);
+  }
   return launch_ring_t<T, OP, VPT, MAXT, kAligned>(a, pl, stage, sms, dev, st);
 }
 
@@ -1027,12 +1031,19 @@ cudaError_t launch_op(const RowQuantArgs& a, cudaStream_t st) {
     return vec ? launch_block_rows<T, OP, kAligned16>(a, pl, st) : launch_block_rows<T, OP, kWindows>(a, pl, st);
   }
   const size_t stage = stage_bytes(shape);
+  // What plan_ring gives: one chunk for more than 384 threads only in fp32, where the
+  // rings of two inputs leave an SM too few threads with more; and four only up to
+  // 384 threads and never whole where two fp32 rows are in a stage.
+  constexpr bool kWide = T::kWords == 8, kTwoWide = kWide && OP == 1;
   if (pl.vpt == 1 && pl.tpr <= 384) return launch_ring<T, OP, 1, 384>(a, pl, stage, sms, dev, st);
-  if (pl.vpt == 1) return launch_ring<T, OP, 1, 1024>(a, pl, stage, sms, dev, st);
+  if constexpr (kWide)
+    if (pl.vpt == 1) return launch_ring<T, OP, 1, 1024>(a, pl, stage, sms, dev, st);
   if (pl.vpt == 2 && pl.tpr <= 384) return launch_ring<T, OP, 2, 384>(a, pl, stage, sms, dev, st);
   if (pl.vpt == 2) return launch_ring<T, OP, 2, 1024>(a, pl, stage, sms, dev, st);
-  if (pl.tpr <= 384) return launch_ring<T, OP, 4, 384>(a, pl, stage, sms, dev, st);
-  return launch_ring<T, OP, 4, 1024>(a, pl, stage, sms, dev, st);
+  if (pl.vpt == 4 && pl.tpr <= 384) return launch_ring<T, OP, 4, 384>(a, pl, stage, sms, dev, st);
+  if constexpr (!kTwoWide)
+    if (pl.vpt == 4) return launch_ring<T, OP, 4, 1024>(a, pl, stage, sms, dev, st);
+  return cudaErrorInvalidConfiguration;
 }
 
 template <class T>
