@@ -403,6 +403,28 @@ __device__ __forceinline__ void tmem_wait_ld_x32(uint32_t (&v)[32]) {
                : "memory");
 }
 
+// ---------------------------------------------------------------- shared memory, codes
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Adding this to |v| < 2^22 leaves v, rounded to an integer, in the low mantissa bits.
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+
+// Low bytes of four rounded values packed into one word.
+__device__ __forceinline__ uint32_t pack_bytes4(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3) {
+  return __byte_perm(__byte_perm(t0, t1, 0x0040), __byte_perm(t2, t3, 0x0040), 0x5410);
+}
+
 // ---------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor for a K-major operand stored in the
 // 128-byte-swizzled canonical layout: rows of 128 bytes, 8-row atoms of 1024

@@ -125,14 +125,6 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
 
 // ------------------------------------------------------------------ few tokens
 constexpr int kFewWarps = 8;
@@ -668,10 +660,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             const uint32_t to = stg + (uint32_t)(lane * kStagePitch + (ch % kGroup * 32 + 8 * j) * (int)sizeof(typename O::elem));
             if constexpr (sizeof(typename O::elem) == 2) {
-              st_shared_v4(to, O::pack(y[0], y[1]), O::pack(y[2], y[3]), O::pack(y[4], y[5]), O::pack(y[6], y[7]));
+              st_shared_v4(to, make_uint4(O::pack(y[0], y[1]), O::pack(y[2], y[3]), O::pack(y[4], y[5]), O::pack(y[6], y[7])));
             } else {
-              st_shared_v4(to, __float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
-              st_shared_v4(to + 16, __float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7]));
+              st_shared_v4(to, make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])));
+              st_shared_v4(to + 16, make_uint4(__float_as_uint(y[4]), __float_as_uint(y[5]), __float_as_uint(y[6]), __float_as_uint(y[7])));
             }
           }
           if (ch % kGroup == kGroup - 1) {

@@ -32,8 +32,6 @@ unsigned int* device_error_word();
 
 namespace {
 
-constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -47,11 +45,6 @@ __device__ __forceinline__ uint32_t pack_nibbles8(const uint32_t (&t)[8]) {
   uint32_t e = __byte_perm(t[5], t[7], 0x5410);
   uint32_t f = (d & 0x000F000Fu) | ((e << 4) & 0x00F000F0u);
   return __byte_perm(c, f, 0x6420);
-}
-
-// Low bytes of four rounded values packed into one word.
-__device__ __forceinline__ uint32_t pack_bytes4(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3) {
-  return __byte_perm(__byte_perm(t0, t1, 0x0040), __byte_perm(t2, t3, 0x0040), 0x5410);
 }
 
 constexpr int kStages = 2;  // stages (blocks of rows) per CTA, both requested up front

@@ -34,8 +34,6 @@ unsigned int* device_error_word();
 
 namespace {
 
-constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-
 struct Bf16 {
   using word = uint16_t;
   static constexpr int kWords = 4;     // 32-bit words of 8 elements
@@ -246,10 +244,6 @@ __device__ __forceinline__ void rotate8(float2 (&f)[4], int group, int lane) {
       }
     }
   }
-}
-
-__device__ __forceinline__ uint32_t pack_bytes4(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3) {
-  return __byte_perm(__byte_perm(t0, t1, 0x0040), __byte_perm(t2, t3, 0x0040), 0x5410);
 }
 
 // Codes of 8 elements: each times 1 / s (`inv`), rounded to the nearest integer
