@@ -383,7 +383,9 @@ def w8a8_matmul(Xq, x_scale, Wq, w_scale, group=0, bias=None, Y=None, dtype=None
     """The int8 product with token and channel scales for any sizes: Y [M, N] =
     ((Xq Wq^T * x_scale) * w_scale) / group + bias in bf16, fp16 or fp32 (the
     type of Y, else `dtype`, else bf16; the bias is of the same type).  Code
-    matrices have rows a multiple of 16 bytes apart, Y rows of any stride."""
+    matrices have rows a multiple of 16 bytes apart, Y rows of any stride.
+    Where w8a8_gemm takes the sizes too, it is the faster one from about 1000
+    tokens on, this one below."""
     if _calls is None:
         _bind_calls()
     dev = Xq.get_device()

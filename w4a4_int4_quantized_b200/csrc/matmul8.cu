@@ -26,10 +26,11 @@
 //   tcgen05.mma kind::i8 in its pair form: each CTA holds 128 rows of A and
 //   BN / 2 of B per stage, 128 bytes of k wide in the 128-byte swizzle that
 //   TMA writes.  Two accumulators of BN columns in tensor memory let the epilogue
-//   of one tile run under the products of the next.  8192 x 24576 x 8192: 1023 to 1055
-//   us alone, 3130 to 3230 TOPS; 4608 x 4096 x 4096: 53 us; 8192 x 4096 x 256, bound by
-//   its epilogues (3.1 us a tile; staged as int32 and scaled on the way out they took
-//   5.2): 25 us.  TMA fills what lies past M, N or K with zeros.
+//   of one tile run under the products of the next.  8192 x 24576 x 8192: 1045 us
+//   from a cool start, 1207 to 1275 in passes that last seconds (2590 to 2730 TOPS; the
+//   power cap decides, and codes uniform over int8 take 1575); 4608 x 4096 x 4096: 53 us;
+//   8192 x 4096 x 256, bound by its epilogues (3.1 us a tile; staged as int32 and scaled
+//   on the way out they took 5.2): 25.6 us.  TMA fills what lies past M, N or K with zeros.
 //     warp 0       TMA loads (both CTAs; both complete on the even CTA's
 //                  barrier)
 //     warp 1       MMA issue (even CTA)
@@ -1127,7 +1128,7 @@ void consider_streamed(const Matmul8Args& a, int sms, int dev, const int* given,
 // The pair kernel.  A k-block costs 0.28 (256 x 128) or 0.30 (256 x 256), a launch
 // 4.7 or 5.8, a split 1.75; whole tiles walk in rounds of SMs / 2, none of which is shorter
 // than its epilogue: 1.75 or 3.1.  Clusters that are not all resident at once would
-// cost a second round (256 x 4096 x 12288 in quarters 34 us, in thirds 19.4), so they
+// cost a second round (256 x 4096 x 12288 in quarters 34 us, in thirds 20), so they
 // are not considered.
 template <int BN, class O>
 void consider_tiled(const Matmul8Args& a, int sms, int dev, const int* given, Form& best) {
@@ -1151,7 +1152,7 @@ void consider_tiled(const Matmul8Args& a, int sms, int dev, const int* given, Fo
 // streamed 22.1 (pair tiles 33); 64, 4096 x 4096 streamed in quarters 8.0 (11); 256,
 // 1024 x 1024 streamed 5.1 (7.0); 333, 1013 x 2995 streamed 7.7 (9.3); 333, 4096 x
 // 12288 pair tiles in halves 22.5 (streamed 27.5); 1000, 14336 x 4096 pair tiles 51
-// (65); 7404, 18199 x 27 pair tiles 114 (180).
+// (65); 7404, 18199 x 27 pair tiles 123 (180).
 template <class O>
 Form choose_form(const Matmul8Args& a, int sms, int dev, const int* given) {
   // Few tokens (us against the best streamed form).  Up to 8, with 52 MB of weights and

@@ -728,10 +728,13 @@ __host__ __device__ __forceinline__ uint32_t slot_bytes(uint32_t row_bytes, bool
 // Many rows: persistent blocks, each row's inputs brought into a ring of
 // `stages` rows in shared memory by bulk copies, so that the next rows arrive
 // while one is worked on and no register holds a load in flight.  A team of tpr
-// threads owns a ring; with rows of one warp a block has several.  Bound by issue
-// slots (19 instructions per element of a norm, 29 with the rotation; 16 and 25 of
-// a gate) before HBM: 16384 x 8192 bf16 norm with residual 156 us, 6.0 TB/s (92% of
-// the copy rate); 4608 x 12288 bf16 gate 48 us, 5.9 TB/s, rotated 64 us.  kShifted
+// threads owns a ring; with rows of one warp a block has several.  Long rows run at
+// HBM's rate: 16384 x 8192 bf16 norm with residual 157 us, 6.0 TB/s (91% of the copy
+// rate); 4608 x 12288 bf16 gate 48 us, 5.9 TB/s.  The others are bound by latency, with
+// a third of the warps resident and issue slots 46 to 59% active: 19 instructions per
+// element of a norm (loads and the two reductions' barriers wait), 29 with the rotation
+// (its shuffles), 14 and 23 of a gate (64 us rotated); and by the last round: 4608 rows
+// over 888 rings are 5.2 rounds, run as 6.  kShifted
 // copies whole 16-byte granules, so a row brings up to 14 bytes of its
 // neighbours along; the first and the last row, which have none on one side,
 // are read from global memory element by element.
@@ -743,7 +746,9 @@ __global__ void __launch_bounds__(MAXT, MAXT < kRingThreads ? kRingThreads / MAX
     row_ring_kernel(RowQuantArgs p, int tpr, int stages, unsigned int* err) {
   using W = typename T::word;
   constexpr bool FULL = LAY == kWhole;
-  // the weights of a thread's elements stay in registers, packed, where they fit
+  // The weights of a thread's elements are loaded once and held packed.  They do not all
+  // fit beside the row in the 80 registers that 768 threads leave: bf16 rows of four
+  // chunks spill 156 bytes a thread to the stack, fp16 56 (27 of the 158 row kernels spill).
   constexpr bool kHoldGamma = OP == 0 && T::kWords == 4 && MAXT < 1024 && LAY != kShifted;
   extern __shared__ __align__(128) uint8_t ring_raw[];
   __shared__ RowShared sh;
