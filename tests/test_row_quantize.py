@@ -16,8 +16,8 @@ Tolerances, with u = 2^-24 (half a step of fp32, relative):
   rotation  a sum of g values in log2 g roundings: at most (c + log2 g) u of
         the group's sum of |y|.
 With D the largest such error of a row, the scale is off by at most
-D / 127 + u s, and y / s by at most 2 * 127 D / max|y| + 4 * 127 u (1 / s by
-rcp.approx 2 u, s and the factor 1 u each), so a code is within half a step plus
+D / 127 + u s, and y / s by at most 2 * 127 D / max|y| + 4 * 127 u (1 / s
+2 u at most, s and the factor 1 u each), so a code is within half a step plus
 that of the 64-bit quotient."""
 from __future__ import annotations
 
@@ -610,3 +610,18 @@ def test_each_refusal_of_the_binding_has_its_status():
         assert e.value.status == status, (kw.keys(), e.value)
     torch.cuda.synchronize()
     assert not code.any() and not s.any()
+
+
+@gpu
+@pytest.mark.parametrize("M,K,group", [(7, 128, 64), (400, 1024, 128), (3000, 3200, 128)])
+def test_strongly_negative_gates_in_fp16_and_rotated(M, K, group):
+    """Rows whose gates all lie below -87: y is some 1e-35, its scale under 2^-100."""
+    import torch
+    rng = np.random.default_rng(92)
+    base = rng.uniform(-96.0, -92.0, (M, 1))
+    gate = _rows(base + rng.uniform(-4.0, 4.0, (M, K)), torch.float16)
+    up = _rows(rng.choice([-1.0, 1.0], (M, K)) * rng.uniform(2e4, 6.5e4, (M, K)), torch.float16)
+    q, s = w4.w8a8_silu_mul_quantize(gate, up, group)
+    torch.cuda.synchronize()
+    a, b = _f64(gate), _f64(up)
+    check_codes(silu64(a, b), group, silu_c(a), _f64(q), _f64(s))
